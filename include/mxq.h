@@ -341,6 +341,88 @@ mxq_status grouped_wgrad_mx(const uint8_t* a_q, const uint8_t* a_s, const uint8_
                             const int64_t* group_offsets, int64_t G, int64_t M, int64_t N, int64_t Kt,
                             uint16_t* c_bf16, float* c_f32, hipStream_t stream);
 
+/*
+ * RMSNorm with the residual's addition and an MXFP8 output: the norm in front of an MXFP8 projection writes that
+ * projection's operands ([OLMO11] Section 11.2.1, Eq. 58, and Section 11.3.2, Eq. 60: the row orientation feeds the
+ * forward product, the column orientation its Wgrad), and an 8-bit checkpoint of its input for the backward.
+ *   h = bf16_rne(x + residual), written to sum_bf16; h = x when residual_bf16 is NULL (sum_bf16 must then be NULL too);
+ *   rstd[r] = 1 / sqrt((sum_c h^2) / cols + eps) in fp32 (the order of the sum is the kernel's; a row whose squares
+ *             overflow fp32 has rstd = 0), y = (h rstd) gamma, each operation one fp32 rounding;
+ *   row:        q_row[rows][cols], s_row[rows][cols/32]: y quantized from fp32 as mxq_quantize does;
+ *   column:     q_col[cols][rows], s_col[cols][rows/32]: the same down columns (needs rows % 32 == 0);
+ *   checkpoint: ck_q[rows][cols], ck_s[rows][cols/32]: mxq_quantize's row orientation of h.
+ * Either orientation may be NULL, not both; the checkpoint may be NULL; rstd[rows] is required. sum_bf16 may be x_bf16
+ * or residual_bf16 itself (in place). gamma[cols] is fp32 (the master weight). 0 < eps < 3e38
+ * (MXQ_ERR_UNSUPPORTED otherwise). Requires cols % 32 == 0 and cols <= 32768. A NaN or infinity in a row makes the
+ * row's y NaN where the formula does; its blocks then carry NaN codes and the scale byte 0xFF.
+ */
+mxq_status rmsnorm_mx_quantize(const uint16_t* x_bf16, const uint16_t* residual_bf16, const float* gamma,
+                               int64_t rows, int64_t cols, float eps, uint16_t* sum_bf16, float* rstd, uint8_t* q_row,
+                               uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, uint8_t* ck_q, uint8_t* ck_s,
+                               mxq_scale_rule rule, hipStream_t stream);
+
+/*
+ * Backward of rmsnorm_mx_quantize from its 8-bit checkpoint. With h^ the values of (ck_q, ck_s), xh = h^ rstd,
+ * g = dy gamma and m = (sum_c g xh) / cols (fp32):
+ *   dx[r][c] = bf16_rne(dsum + rstd (g - xh m)), the gradient of x and of the residual alike; dsum_bf16 is the gradient
+ *              that reaches h from the residual stream (NULL: none);
+ *   dgamma[c] = sum_r dy xh (fp32[cols]; accumulate != 0: dgamma += that sum). NULL skips it.
+ * The exact rstd of the forward is kept, so the checkpoint's rounding enters dx only through the projection term xh m.
+ * A block whose scale byte is 0xFF reads back as NaN. The partial sums of dgamma are added in a fixed order. dx_bf16
+ * may be dy_bf16 or dsum_bf16 itself (in place). workspace: mxq_workspace_bytes("rmsnorm_backward", cols) bytes,
+ * clobbered (needed only for dgamma). With rows == 0, dgamma is zeroed (or left alone when accumulating).
+ */
+mxq_status rmsnorm_backward_mx_checkpoint(const uint16_t* dy_bf16, const uint16_t* dsum_bf16, const uint8_t* ck_q,
+                                          const uint8_t* ck_s, const float* rstd, const float* gamma, int64_t rows,
+                                          int64_t cols, uint16_t* dx_bf16, float* dgamma, int accumulate,
+                                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * swiglu_mx_quantize that also writes an 8-bit checkpoint of its input c (33/32 bytes a value in place of 2), from
+ * which swiglu_backward_mx_checkpoint computes the gradients and the down projection's Wgrad operand:
+ *   q[rows][F], s[rows][F/32]: as swiglu_mx_quantize, from the bf16 c;
+ *   ck_q[rows][2F], ck_s[rows][2F/32]: mxq_quantize's row orientation of c.
+ * Requires F % 32 == 0.
+ */
+mxq_status swiglu_mx_quantize_checkpoint(const uint16_t* c_bf16, int64_t rows, int64_t F, uint8_t* q, uint8_t* s,
+                                         uint8_t* ck_q, uint8_t* ck_s, mxq_scale_rule rule, hipStream_t stream);
+
+/*
+ * swiglu_backward_mx_quantize from the 8-bit checkpoint: c^ = (g | u), the values of (ck_q, ck_s), in place of c.
+ *   q_row, s_row, q_col, s_col: dc as in swiglu_backward_mx_quantize (rows of 2F; blocks of 32 rows down columns);
+ *   h_q_col[F][rows], h_s_col[F][rows/32]: h = silu(g) u recomputed from the checkpoint, column orientation, so the
+ *   forward need not keep the down projection's Wgrad operand.
+ * Each pair may be NULL, not all three. A block whose scale byte is 0xFF reads back as NaN. Requires F % 32 == 0, and
+ * rows % 32 == 0 when a column orientation is asked for.
+ */
+mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_s, const uint16_t* dh_bf16,
+                                         int64_t rows, int64_t F, uint8_t* q_row, uint8_t* s_row, uint8_t* q_col,
+                                         uint8_t* s_col, uint8_t* h_q_col, uint8_t* h_s_col, mxq_scale_rule rule,
+                                         hipStream_t stream);
+
+/*
+ * The routed experts of a few tokens (1 <= tokens <= 64; 0 is empty) in two launches, with no dispatch and no padding
+ * to 32 rows an expert: for decoding and for small evaluation batches. Per token t:
+ *   the topk largest logits (fp32[tokens][experts]) choose its experts, equal logits by the lower index; p = the softmax
+ *   of the chosen logits (normalize != 0) or their share of the softmax over all logits (normalize == 0);
+ *   c = bf16_rne(x W_up[e]^T), h = swiglu_mx_quantize(c) (rceil), y[t] = bf16_rne(sum_e p_e (h W_down[e]^T)),
+ * the products on the values the MXFP8 operands stand for, with fp32 accumulation and bf16-exact factors: the
+ * arithmetic of grouped_scaled_gemm and swiglu_mx_quantize, so decoding sees the numbers of the training forward.
+ *   x_q[tokens][D], x_s[tokens][D/32]; w_up_q[experts][2F][D] (gate rows, then up rows), w_up_s[experts][2F][D/32];
+ *   w_down_q[experts][D][F], w_down_s[experts][D][F/32]: the row-orientation weight caches; y_bf16[tokens][D].
+ * A logit of -inf is never chosen (a token with fewer than topk finite logits uses those; one with none gets a row of
+ * zeros); a NaN or +inf among a token's logits makes its row NaN. Results do not depend on timing.
+ * Requires experts <= 1024, 1 <= topk <= min(experts, 32), D and F positive multiples of 32 up to 2^20. workspace:
+ * moe_mx_few_tokens_workspace_bytes(tokens, experts, topk, F) bytes, clobbered; that call returns 0 for sizes out of
+ * range.
+ */
+mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float* logits, int64_t tokens,
+                             int64_t experts, int64_t topk, int normalize, const uint8_t* w_up_q,
+                             const uint8_t* w_up_s, const uint8_t* w_down_q, const uint8_t* w_down_s, int64_t D,
+                             int64_t F, uint16_t* y_bf16, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t F);
+
 /* Adam hyper-parameters, passed by HOST pointer. step is the 1-based step count t (MXQ_ERR_SHAPE if below 1);
  * beta1 and beta2 lie in [0, 1) (MXQ_ERR_UNSUPPORTED otherwise, NaN included). Every Adam entry point checks both
  * before its early return for an empty tensor, so a call with n == 0 still reports a bad setting. */
@@ -397,7 +479,7 @@ mxq_status fp8_adam_step_delayed(float* master, const uint16_t* grad_bf16, uint8
                                  size_t workspace_bytes, hipStream_t stream);
 
 /* Workspace bytes needed by op ("pertensor", "adam", "pertensor_delayed", "adam_delayed" or "autoscale") for n
- * elements; 0 for an unknown op. op is a host string. */
+ * elements, or by "rmsnorm_backward" for n columns; 0 for an unknown op. op is a host string. */
 size_t mxq_workspace_bytes(const char* op, int64_t n);
 
 #ifdef __cplusplus

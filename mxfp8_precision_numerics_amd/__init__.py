@@ -11,6 +11,12 @@ outputs, and call the C ABI of libmxq.so with raw pointers. All arithmetic happe
   fp8_adam_step          precision-decoupled FP8 AdamW step (fp32 master, E4M3 m + scale, fp16 v, bf16 copy)
   swiglu_mx_quantize(_oriented), swiglu_backward_mx_quantize, route_weighted_mx_quantize
                          the routed MLP's fused elementwise + MX quantize steps (forward and backward)
+  rmsnorm_mx_quantize, rmsnorm_backward_mx_checkpoint
+                         RMSNorm with the residual's addition and an MXFP8 output, and its backward from an 8-bit
+                         checkpoint of its input
+  swiglu_mx_quantize_checkpoint, swiglu_backward_mx_checkpoint
+                         SwiGLU + MX quantize with an 8-bit checkpoint of its input, and its backward from it
+  moe_mx_few_tokens      the routed experts of up to 64 tokens, from router logits to the weighted sum
 """
 from __future__ import annotations
 
@@ -25,6 +31,8 @@ from ._lib import E4M3, E5M2, FLOOR, MX_BLOCK32, PER_TENSOR, RCEIL, AdamHParams,
 __all__ = ["mx_quantize", "mx_quantize_ranged", "pertensor_quantize", "scaled_gemm", "scaled_gemm_ranged", "grouped_scaled_gemm", "fp8_adam_step",
            "swiglu_mx_quantize", "swiglu_mx_quantize_oriented", "swiglu_backward_mx_quantize", "route_weighted_mx_quantize",
            "grouped_scaled_gemm_strided", "grouped_wgrad_mx",
+           "rmsnorm_mx_quantize", "rmsnorm_backward_mx_checkpoint", "swiglu_mx_quantize_checkpoint",
+           "swiglu_backward_mx_checkpoint", "moe_mx_few_tokens", "RMSNormOut",
            "workspace_bytes", "MXTensor", "AdamHParams", "MXQError", "E4M3", "E5M2", "RCEIL", "FLOOR",
            "PER_TENSOR", "MX_BLOCK32"]
 
@@ -444,3 +452,181 @@ def fp8_requantize_shared(q: torch.Tensor, fmt_in: int, scale_in: torch.Tensor, 
                                            _stream(dev))
     _lib.check("fp8_requantize_shared", st)
     return out, sg, ssum
+
+
+class RMSNormOut(NamedTuple):
+    mx: MXTensor                        # MXFP8 of the normalized values, in the requested orientations
+    sum: Optional[torch.Tensor]         # bf16 [rows][cols]: x + residual (None without a residual)
+    rstd: torch.Tensor                  # float32[rows]
+    checkpoint: Optional[MXTensor]      # MXFP8 row orientation of the norm's input (q_col and s_col None)
+
+
+def _expect(t: Optional[torch.Tensor], shape, dtype, dev, name: str):
+    """A buffer of exactly this shape, type and device, contiguous."""
+    if t is None or tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {dev}")
+
+
+def _expect_mx(mx: MXTensor, rows: int, cols: int, dev, name: str):
+    """The pairs of mx that are there hold an MXFP8 [rows][cols]."""
+    for q, s, a, b, o in ((mx.q_row, mx.s_row, rows, cols, "row"), (mx.q_col, mx.s_col, cols, rows, "col")):
+        if q is None and s is None:
+            continue
+        _expect(q, (a, b), torch.uint8, dev, f"{name}.q_{o}")
+        _expect(s, (a, b // 32), torch.uint8, dev, f"{name}.s_{o}")
+
+
+def rmsnorm_mx_quantize(x: torch.Tensor, gamma: torch.Tensor, eps: float, residual: Optional[torch.Tensor] = None,
+                        rowwise: bool = True, colwise: bool = True, checkpoint: bool = True, rule: int = RCEIL,
+                        out: Optional[RMSNormOut] = None) -> RMSNormOut:
+    """RMSNorm of x (+ residual), bf16 [rows][cols], with gamma float32[cols], straight into MXFP8 of y = h rstd gamma
+    in the requested orientations, plus h = bf16(x + residual) when a residual is given, rstd, and the 8-bit checkpoint
+    of h that rmsnorm_backward_mx_checkpoint reads. `out` reuses caller buffers (out.sum may be x or residual)."""
+    _dev(x, torch.bfloat16, "x"); _dev(gamma, torch.float32, "gamma")
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][cols]")
+    rows, cols = x.shape
+    dev = x.device
+    if tuple(gamma.shape) != (cols,) or gamma.device != dev:
+        raise ValueError("gamma must hold one value per column of x, on x's device")
+    if residual is not None:
+        _dev(residual, torch.bfloat16, "residual")
+        _expect(residual, (rows, cols), torch.bfloat16, dev, "residual")
+    if out is None:
+        out = RMSNormOut(_mx_out(rows, cols, rowwise, colwise, dev), None if residual is None else torch.empty_like(x),
+                         torch.empty(rows, dtype=torch.float32, device=dev),
+                         _mx_out(rows, cols, True, False, dev) if checkpoint else None)
+    else:
+        _expect_mx(out.mx, rows, cols, dev, "out.mx")
+        _expect(out.rstd, (rows,), torch.float32, dev, "out.rstd")
+        if residual is not None:
+            _expect(out.sum, (rows, cols), torch.bfloat16, dev, "out.sum")
+        if out.checkpoint is not None:
+            _expect_mx(out.checkpoint, rows, cols, dev, "out.checkpoint")
+    ck = out.checkpoint if out.checkpoint is not None else MXTensor(None, None, None, None)
+    st = _lib.load().rmsnorm_mx_quantize(_ptr(x), _ptr(residual), _ptr(gamma), rows, cols, C.c_float(eps),
+                                         _ptr(out.sum) if residual is not None else None, _ptr(out.rstd),
+                                         _ptr(out.mx.q_row), _ptr(out.mx.s_row), _ptr(out.mx.q_col),
+                                         _ptr(out.mx.s_col), _ptr(ck.q_row), _ptr(ck.s_row), rule, _stream(dev))
+    _lib.check("rmsnorm_mx_quantize", st)
+    return out
+
+
+def rmsnorm_backward_mx_checkpoint(dy: torch.Tensor, checkpoint: MXTensor, rstd: torch.Tensor, gamma: torch.Tensor,
+                                   residual_grad: Optional[torch.Tensor] = None, want_dgamma: bool = True,
+                                   accumulate: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                   workspace: Optional[torch.Tensor] = None):
+    """(dx, dgamma) of the norm from its 8-bit checkpoint (row orientation) and rstd. dx (bf16) includes residual_grad,
+    the gradient arriving on the residual stream. dgamma is a new float32[cols], or is added into `accumulate`; None
+    with want_dgamma=False. `out` may be dy or residual_grad."""
+    _dev(dy, torch.bfloat16, "dy"); _dev(rstd, torch.float32, "rstd"); _dev(gamma, torch.float32, "gamma")
+    if dy.dim() != 2:
+        raise ValueError("dy must be [rows][cols]")
+    rows, cols = dy.shape
+    dev = dy.device
+    _expect(checkpoint.q_row, (rows, cols), torch.uint8, dev, "checkpoint.q_row")
+    _expect(checkpoint.s_row, (rows, cols // 32), torch.uint8, dev, "checkpoint.s_row")
+    _expect(rstd, (rows,), torch.float32, dev, "rstd")
+    _expect(gamma, (cols,), torch.float32, dev, "gamma")
+    if residual_grad is not None:
+        _expect(residual_grad, (rows, cols), torch.bfloat16, dev, "residual_grad")
+    if out is None:
+        out = torch.empty_like(dy)
+    else:
+        _expect(out, (rows, cols), torch.bfloat16, dev, "out")
+    dgamma = accumulate
+    if accumulate is not None:
+        _expect(accumulate, (cols,), torch.float32, dev, "accumulate")
+    elif want_dgamma:
+        dgamma = torch.empty(cols, dtype=torch.float32, device=dev)
+    if dgamma is not None and workspace is None:
+        workspace = torch.empty(workspace_bytes("rmsnorm_backward", cols), dtype=torch.uint8, device=dev)
+    st = _lib.load().rmsnorm_backward_mx_checkpoint(
+        _ptr(dy), _ptr(residual_grad), _ptr(checkpoint.q_row), _ptr(checkpoint.s_row), _ptr(rstd), _ptr(gamma), rows,
+        cols, _ptr(out), _ptr(dgamma), 1 if accumulate is not None else 0, _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _stream(dev))
+    _lib.check("rmsnorm_backward_mx_checkpoint", st)
+    return out, dgamma
+
+
+def swiglu_mx_quantize_checkpoint(c: torch.Tensor, rule: int = RCEIL, out=None):
+    """c: bf16 [rows][2F] (gate | up) -> (MXFP8 row orientation of silu(gate) * up, MXFP8 row orientation of c): the
+    down projection's operand and the checkpoint that swiglu_backward_mx_checkpoint reads. `out` reuses a pair of
+    MXTensors."""
+    _dev(c, torch.bfloat16, "c")
+    rows, f2 = c.shape
+    F = f2 // 2
+    if f2 != 2 * F:
+        raise ValueError("c must be [rows][2F]")
+    if out is None:
+        out = (_mx_out(rows, F, True, False, c.device), _mx_out(rows, f2, True, False, c.device))
+    h, ck = out
+    _expect_mx(h, rows, F, c.device, "out[0]")
+    _expect_mx(ck, rows, f2, c.device, "out[1]")
+    st = _lib.load().swiglu_mx_quantize_checkpoint(_ptr(c), rows, F, _ptr(h.q_row), _ptr(h.s_row), _ptr(ck.q_row),
+                                                   _ptr(ck.s_row), rule, _stream(c.device))
+    _lib.check("swiglu_mx_quantize_checkpoint", st)
+    return h, ck
+
+
+def swiglu_backward_mx_checkpoint(checkpoint: MXTensor, dh: torch.Tensor, rowwise: bool = True, colwise: bool = True,
+                                  hidden: bool = True, rule: int = RCEIL, out=None):
+    """checkpoint: swiglu_mx_quantize_checkpoint's MXFP8 of c [rows][2F]; dh: bf16 [rows][F] -> (MXFP8 of
+    (d_gate | d_up) [rows][2F] in the requested orientations, MXFP8 of silu(gate) * up [rows][F] in the column
+    orientation: the down projection's Wgrad operand, or None with hidden=False). `out` reuses such a pair."""
+    _dev(dh, torch.bfloat16, "dh")
+    rows, F = dh.shape
+    dev = dh.device
+    _expect(checkpoint.q_row, (rows, 2 * F), torch.uint8, dev, "checkpoint.q_row")
+    _expect(checkpoint.s_row, (rows, 2 * F // 32), torch.uint8, dev, "checkpoint.s_row")
+    if out is None:
+        out = (_mx_out(rows, 2 * F, rowwise, colwise, dev), _mx_out(rows, F, False, True, dev) if hidden else None)
+    dc, h = out
+    _expect_mx(dc, rows, 2 * F, dev, "out[0]")
+    if h is not None:
+        _expect_mx(h, rows, F, dev, "out[1]")
+    st = _lib.load().swiglu_backward_mx_checkpoint(
+        _ptr(checkpoint.q_row), _ptr(checkpoint.s_row), _ptr(dh), rows, F, _ptr(dc.q_row), _ptr(dc.s_row),
+        _ptr(dc.q_col), _ptr(dc.s_col), None if h is None else _ptr(h.q_col), None if h is None else _ptr(h.s_col),
+        rule, _stream(dev))
+    _lib.check("swiglu_backward_mx_checkpoint", st)
+    return dc, h
+
+
+def moe_few_tokens_workspace_bytes(tokens: int, experts: int, topk: int, F: int) -> int:
+    return int(_lib.load().moe_mx_few_tokens_workspace_bytes(int(tokens), int(experts), int(topk), int(F)))
+
+
+def moe_mx_few_tokens(x_q: torch.Tensor, x_s: torch.Tensor, logits: torch.Tensor, topk: int, w_up_q: torch.Tensor,
+                      w_up_s: torch.Tensor, w_down_q: torch.Tensor, w_down_s: torch.Tensor, normalize: bool = True,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The routed experts of up to 64 tokens: x MXFP8 [tokens][D], logits float32 [tokens][experts], w_up MXFP8
+    [experts][2F][D] (gate rows, then up rows), w_down MXFP8 [experts][D][F] (row orientation) -> bf16 [tokens][D], the
+    softmax-weighted sum over each token's topk experts (weights over the chosen experts, or with normalize=False over
+    all)."""
+    for t, n in ((x_q, "x_q"), (x_s, "x_s"), (w_up_q, "w_up_q"), (w_up_s, "w_up_s"), (w_down_q, "w_down_q"),
+                 (w_down_s, "w_down_s")):
+        _dev(t, torch.uint8, n)
+    _dev(logits, torch.float32, "logits")
+    if x_q.dim() != 2 or logits.dim() != 2 or w_up_q.dim() != 3:
+        raise ValueError("x_q must be [tokens][D], logits [tokens][experts], w_up_q [experts][2F][D]")
+    T, D = x_q.shape
+    E, F = logits.shape[1], w_up_q.shape[1] // 2
+    dev = x_q.device
+    _expect(x_s, (T, D // 32), torch.uint8, dev, "x_s")
+    _expect(logits, (T, E), torch.float32, dev, "logits")
+    _expect(w_up_q, (E, 2 * F, D), torch.uint8, dev, "w_up_q")
+    _expect(w_up_s, (E, 2 * F, D // 32), torch.uint8, dev, "w_up_s")
+    _expect(w_down_q, (E, D, F), torch.uint8, dev, "w_down_q")
+    _expect(w_down_s, (E, D, F // 32), torch.uint8, dev, "w_down_s")
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.bfloat16, device=dev)
+    else:
+        _expect(out, (T, D), torch.bfloat16, dev, "out")
+    if workspace is None:
+        workspace = torch.empty(moe_few_tokens_workspace_bytes(T, E, topk, F), dtype=torch.uint8, device=dev)
+    st = _lib.load().moe_mx_few_tokens(_ptr(x_q), _ptr(x_s), _ptr(logits), T, E, topk, 1 if normalize else 0,
+                                       _ptr(w_up_q), _ptr(w_up_s), _ptr(w_down_q), _ptr(w_down_s), D, F, _ptr(out),
+                                       _ptr(workspace), workspace.numel(), _stream(dev))
+    _lib.check("moe_mx_few_tokens", st)
+    return out

@@ -14,7 +14,8 @@ LIB = os.path.join(PKG, "libmxq.so")
 PROBE_LIB = os.path.join(PKG, "libmxq_probe.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
-SOURCES = ["quantize.hip", "gemm.hip", "adam.hip", "gradcomm.hip", "moe.hip", "abi.hip"]
+SOURCES = ["quantize.hip", "gemm.hip", "adam.hip", "gradcomm.hip", "moe.hip", "norm.hip", "checkpoint.hip",
+           "moe_few.hip", "abi.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

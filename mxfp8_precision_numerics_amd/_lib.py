@@ -51,6 +51,12 @@ SIGNATURES = {
     "swiglu_backward_mx_quantize": (_I, [_P, _P, _I64, _I64, _P, _P, _P, _P, _I, _P]),
     "grouped_scaled_gemm_strided": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P,
                                          _I64, _P]),
+    "rmsnorm_mx_quantize": (_I, [_P, _P, _P, _I64, _I64, _F, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "rmsnorm_backward_mx_checkpoint": (_I, [_P, _P, _P, _P, _P, _P, _I64, _I64, _P, _P, _I, _P, _SZ, _P]),
+    "swiglu_mx_quantize_checkpoint": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _I, _P]),
+    "swiglu_backward_mx_checkpoint": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _P]),
+    "moe_mx_few_tokens": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
+    "moe_mx_few_tokens_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
     "grouped_wgrad_mx": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
 }
 

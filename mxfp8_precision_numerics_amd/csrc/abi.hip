@@ -16,6 +16,8 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 size_t pertensor_ws(int64_t n) { return round_up((size_t)mxq::pertensor_amax_parts(n) * 4u, 256); }
 size_t adam_ws(int64_t n) { return round_up((size_t)mxq::adam_parts(n) * 4u, 256) + 256; }
+// One partial row of dgamma (cols floats) per workgroup of the backward.
+size_t rmsnorm_backward_ws(int64_t cols) { return round_up((size_t)mxq::kNormBwdParts * (size_t)cols * 4u, 256); }
 constexpr size_t kDelayedWs = 256;   // delayed modes: the atomic amax word (and Adam's three constants)
 constexpr int64_t kMaxHistory = 1 << 20;
 
@@ -75,6 +77,7 @@ size_t mxq_workspace_bytes(const char* op, int64_t n) {
     if (!op || n < 0) return 0;
     if (strcmp(op, "pertensor") == 0) return pertensor_ws(n);
     if (strcmp(op, "adam") == 0) return adam_ws(n);
+    if (strcmp(op, "rmsnorm_backward") == 0) return rmsnorm_backward_ws(n);
     if (strcmp(op, "pertensor_delayed") == 0 || strcmp(op, "adam_delayed") == 0 || strcmp(op, "autoscale") == 0)
         return kDelayedWs;
     return 0;
@@ -431,6 +434,112 @@ mxq_status fp8_adam_step_delayed(float* master, const uint16_t* grad_bf16, uint8
     float* consts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + 16);
     return hip_status(mxq::launch_adam_delayed(master, grad_bf16, m_q, m_scale, v_fp16, w_bf16, n, k, m_history,
                                                hist_pos, (int)history_len, consts, amax_word, stream));
+}
+
+}  // extern "C"
+
+extern "C" {
+
+mxq_status rmsnorm_mx_quantize(const uint16_t* x_bf16, const uint16_t* residual_bf16, const float* gamma,
+                               int64_t rows, int64_t cols, float eps, uint16_t* sum_bf16, float* rstd, uint8_t* q_row,
+                               uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, uint8_t* ck_q, uint8_t* ck_s,
+                               mxq_scale_rule rule, hipStream_t stream) {
+    if (rule != MXQ_SCALE_RCEIL && rule != MXQ_SCALE_FLOOR) return MXQ_ERR_UNSUPPORTED;
+    if (!(eps > 0.0f && eps < 3.0e38f)) return MXQ_ERR_UNSUPPORTED;              // NaN fails too
+    if (rows < 0 || cols < 0 || cols % 32 != 0 || cols > mxq::kNormMaxCols) return MXQ_ERR_SHAPE;
+    if ((rows + 127) / 128 > kMaxGridY) return MXQ_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return MXQ_OK;                                   // every pointer may be NULL
+    if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr) ||
+        (ck_q == nullptr) != (ck_s == nullptr) || (residual_bf16 == nullptr) != (sum_bf16 == nullptr))
+        return MXQ_ERR_NULL;
+    if (!q_row && !q_col) return MXQ_ERR_NULL;
+    if (q_col && rows % 32 != 0) return MXQ_ERR_SHAPE;
+    if (!x_bf16 || !gamma || !rstd) return MXQ_ERR_NULL;
+    if (!al16(x_bf16) || !al16(residual_bf16) || !al16(gamma) || !al16(sum_bf16) || !al16(rstd) || !al16(q_row) ||
+        !al16(s_row) || !al16(q_col) || !al16(s_col) || !al16(ck_q) || !al16(ck_s))
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_rmsnorm_mx_quantize(x_bf16, residual_bf16, gamma, rows, cols, eps, sum_bf16, rstd,
+                                                      q_row, s_row, q_col, s_col, ck_q, ck_s, (int)rule, stream));
+}
+
+mxq_status rmsnorm_backward_mx_checkpoint(const uint16_t* dy_bf16, const uint16_t* dsum_bf16, const uint8_t* ck_q,
+                                          const uint8_t* ck_s, const float* rstd, const float* gamma, int64_t rows,
+                                          int64_t cols, uint16_t* dx_bf16, float* dgamma, int accumulate,
+                                          void* workspace, size_t workspace_bytes, hipStream_t stream) {
+    if (rows < 0 || cols < 0 || cols % 32 != 0 || cols > mxq::kNormMaxCols) return MXQ_ERR_SHAPE;
+    if (cols == 0) return MXQ_OK;
+    if (rows > 0 && (!dy_bf16 || !ck_q || !ck_s || !rstd || !gamma || !dx_bf16)) return MXQ_ERR_NULL;
+    if (!al16(dy_bf16) || !al16(dsum_bf16) || !al16(ck_q) || !al16(ck_s) || !al16(rstd) || !al16(gamma) ||
+        !al16(dx_bf16) || !al16(dgamma))
+        return MXQ_ERR_ALIGN;
+    if (dgamma) {
+        if (!workspace || workspace_bytes < rmsnorm_backward_ws(cols)) return MXQ_ERR_WORKSPACE;
+        if (!al16(workspace)) return MXQ_ERR_ALIGN;
+    } else if (rows == 0) {
+        return MXQ_OK;
+    }
+    return hip_status(mxq::launch_rmsnorm_backward(dy_bf16, dsum_bf16, ck_q, ck_s, rstd, gamma, rows, cols, dx_bf16,
+                                                   dgamma, accumulate ? 1 : 0, static_cast<float*>(workspace),
+                                                   stream));
+}
+
+mxq_status swiglu_mx_quantize_checkpoint(const uint16_t* c_bf16, int64_t rows, int64_t F, uint8_t* q, uint8_t* s,
+                                         uint8_t* ck_q, uint8_t* ck_s, mxq_scale_rule rule, hipStream_t stream) {
+    if (rule != MXQ_SCALE_RCEIL && rule != MXQ_SCALE_FLOOR) return MXQ_ERR_UNSUPPORTED;
+    if (rows < 0 || F < 0 || F % 32 != 0) return MXQ_ERR_SHAPE;
+    if (rows == 0 || F == 0) return MXQ_OK;
+    if ((F / 8) > (int64_t(1) << 31) || rows > (int64_t(1) << 38) / (F / 8)) return MXQ_ERR_SHAPE;   // the launch grid
+    if (!c_bf16 || !q || !s || !ck_q || !ck_s) return MXQ_ERR_NULL;
+    if (!al16(c_bf16) || !al16(q) || !al16(s) || !al16(ck_q) || !al16(ck_s)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_swiglu_checkpoint(c_bf16, rows, F, q, s, ck_q, ck_s, (int)rule, stream));
+}
+
+mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_s, const uint16_t* dh_bf16,
+                                         int64_t rows, int64_t F, uint8_t* q_row, uint8_t* s_row, uint8_t* q_col,
+                                         uint8_t* s_col, uint8_t* h_q_col, uint8_t* h_s_col, mxq_scale_rule rule,
+                                         hipStream_t stream) {
+    if (rule != MXQ_SCALE_RCEIL && rule != MXQ_SCALE_FLOOR) return MXQ_ERR_UNSUPPORTED;
+    if (rows < 0 || F < 0 || F % 32 != 0) return MXQ_ERR_SHAPE;
+    if ((rows + 63) / 64 > kMaxGridY) return MXQ_ERR_SHAPE;
+    if (rows == 0 || F == 0) return MXQ_OK;                                      // every pointer may be NULL
+    if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr) ||
+        (h_q_col == nullptr) != (h_s_col == nullptr))
+        return MXQ_ERR_NULL;
+    if (!q_row && !q_col && !h_q_col) return MXQ_ERR_NULL;
+    if ((q_col || h_q_col) && rows % 32 != 0) return MXQ_ERR_SHAPE;
+    if (!ck_q || !ck_s || !dh_bf16) return MXQ_ERR_NULL;
+    if (!al16(ck_q) || !al16(ck_s) || !al16(dh_bf16) || !al16(q_row) || !al16(s_row) || !al16(q_col) || !al16(s_col) ||
+        !al16(h_q_col) || !al16(h_s_col))
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_swiglu_bwd_checkpoint(ck_q, ck_s, dh_bf16, rows, F, q_row, s_row, q_col, s_col,
+                                                        h_q_col, h_s_col, (int)rule, stream));
+}
+
+size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t F) {
+    if (tokens < 0 || tokens > mxq::kMoeFewTokens || experts < 1 || experts > mxq::kMoeFewExperts || topk < 1 ||
+        topk > experts || topk > mxq::kMoeFewTopk || F < 0)
+        return 0;
+    return mxq::moe_few_workspace(tokens, experts, topk, F);
+}
+
+mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float* logits, int64_t tokens,
+                             int64_t experts, int64_t topk, int normalize, const uint8_t* w_up_q,
+                             const uint8_t* w_up_s, const uint8_t* w_down_q, const uint8_t* w_down_s, int64_t D,
+                             int64_t F, uint16_t* y_bf16, void* workspace, size_t workspace_bytes,
+                             hipStream_t stream) {
+    if (tokens < 0 || tokens > mxq::kMoeFewTokens || experts < 1 || experts > mxq::kMoeFewExperts || topk < 1 ||
+        topk > experts || topk > mxq::kMoeFewTopk)
+        return MXQ_ERR_SHAPE;
+    if (D < 32 || D % 32 != 0 || F < 32 || F % 32 != 0 || D > (1 << 20) || F > (1 << 20)) return MXQ_ERR_SHAPE;
+    if (tokens == 0) return MXQ_OK;
+    if (!x_q || !x_s || !logits || !w_up_q || !w_up_s || !w_down_q || !w_down_s || !y_bf16) return MXQ_ERR_NULL;
+    if (!al16(x_q) || !al16(x_s) || !al16(logits) || !al16(w_up_q) || !al16(w_up_s) || !al16(w_down_q) ||
+        !al16(w_down_s) || !al16(y_bf16))
+        return MXQ_ERR_ALIGN;
+    if (!workspace || workspace_bytes < mxq::moe_few_workspace(tokens, experts, topk, F)) return MXQ_ERR_WORKSPACE;
+    if (!al16(workspace)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_moe_few(x_q, x_s, logits, w_up_q, w_up_s, w_down_q, w_down_s, tokens, experts, topk,
+                                          D, F, normalize ? 1 : 0, y_bf16, workspace, stream));
 }
 
 }  // extern "C"
