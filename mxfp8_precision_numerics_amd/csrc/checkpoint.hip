@@ -30,8 +30,10 @@ __global__ __launch_bounds__(256) void swiglu_ck_fwd_kernel(const uint16_t* __re
     float g[8], u[8], h[8];
     unpack8(gv, g);
     unpack8(uv, u);
+    float sig[8];
+    silu8(g, h, sig);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] = swiglu_f32(g[e], u[e]);
+    for (int e = 0; e < 8; ++e) h[e] = h[e] * u[e];
     uint32_t bh, bg, bu;
     stnt8(q + r * F + j, encode_row8<RULE>(h, bh));
     stnt8(ck_q + r * 2 * F + j, encode_row8_bf16<RULE>(gv, bg));
@@ -61,19 +63,26 @@ __device__ __forceinline__ void ck_col_out(const float (&x)[4][8], float* tile, 
     }
     __syncthreads();
     const int c = tid & (CT_COLS - 1), b = tid >> 7;
-    float d[32];
-    uint32_t m = 0;
+    float d[32], top = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
+    for (int r = 0; r < 32; r += 2) {
         d[r] = tile[(32 * b + r) * CT_COLS + c];
-        m = max(m, __float_as_uint(d[r]) & 0x7FFFFFFFu);
+        d[r + 1] = tile[(32 * b + r + 1) * CT_COLS + c];
+        top = amax3(top, d[r], d[r + 1]);
     }
     __syncthreads();                                             // the tile may be refilled after this
+    const uint32_t m = __float_as_uint(top) & 0x7FFFFFFFu;
     const uint32_t byte = mx_scale_byte_f32(m, RULE);
-    const float f = mx_inv_scale_f32(byte);
     uint32_t o[8];
+    if (block_is_plain<RULE>(m)) {
+        const float s = scale_operand(byte);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = encode4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3], f);
+        for (int i = 0; i < 8; ++i) o[i] = encode4_plain(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3], s);
+    } else {
+        const float f = mx_inv_scale_f32(byte);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = encode4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3], f);
+    }
     const int64_t grow = r0 + 32 * b;
     if (c0 + c < climit && grow < rows) {
         uint4* q = reinterpret_cast<uint4*>(q_col + (oc0 + c) * rows + grow);
@@ -100,17 +109,6 @@ __device__ __forceinline__ void ck_row_out(const float (&x)[4][8], int64_t r0, i
     }
 }
 
-// sigma = 1 / (1 + e^-g), silu = g / (1 + e^-g), silu' = sigma (1 + g (1 - sigma)); one rounding per operation.
-__device__ __forceinline__ void swiglu_ck_grad(float g, float u, float dh, float& dg, float& du, float& h) {
-    const float d = 1.0f + exp_fixed(-g);
-    const float silu = g / d;
-    const float sig = 1.0f / d;
-    const float ds = sig * (1.0f + g * (1.0f - sig));
-    dg = (dh * u) * ds;
-    du = dh * silu;
-    h = silu * u;
-}
-
 struct CkBwdArgs {
     const uint8_t *ck_q, *ck_s;
     const uint16_t* dh;
@@ -135,8 +133,15 @@ __global__ __launch_bounds__(256) void swiglu_ck_bwd_kernel(CkBwdArgs a) {
             dequant8(ldnt8(a.ck_q + gr * 2 * F + gc), e8m0_value(a.ck_s[gr * (F / 16) + gc / 32]), g);
             dequant8(ldnt8(a.ck_q + gr * 2 * F + F + gc), e8m0_value(a.ck_s[gr * (F / 16) + F / 32 + gc / 32]), u);
             unpack8(ldnt16(a.dh + gr * F + gc), d);
+            // sigma = 1 / (1 + e^-g), silu = g / (1 + e^-g), silu' = sigma (1 + g (1 - sigma))
+            float silu[8], sig[8];
+            silu8(g, silu, sig);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) swiglu_ck_grad(g[e], u[e], d[e], xg[j][e], xu[j][e], xh[j][e]);
+            for (int e = 0; e < 8; ++e) {
+                xg[j][e] = (d[e] * u[e]) * (sig[e] * (1.0f + g[e] * (1.0f - sig[e])));
+                xu[j][e] = d[e] * silu[e];
+                xh[j][e] = silu[e] * u[e];
+            }
         }
     }
     if (a.q_row) {

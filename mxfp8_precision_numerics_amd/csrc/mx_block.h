@@ -44,17 +44,44 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
         clamp_keep_nan(c * f, 448.0f), clamp_keep_nan(d * f, 448.0f));
 }
 
+// The same by the scaled conversion (v_cvt_scalef32_pk_fp8_f32 divides by 2^E, E the exponent field of s): half an
+// instruction a value where the clamped form takes five and a half. It does not saturate, so it serves blocks whose
+// values are finite and at most 448 scales: see block_is_plain.
+__device__ __forceinline__ uint32_t encode4_plain(float a, float b, float c, float d, float s) {
+    v2s o = __builtin_bit_cast(v2s, __builtin_nondeterministic_value(0u));
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, a, b, s, false);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o, c, d, s, true);
+    return __builtin_bit_cast(uint32_t, o);
+}
+
+// The rceil rule's scale keeps every finite value of a block within 448 scales. Blocks at the ends of the exponent range
+// (all zero, below 2^-119, holding an infinity or a NaN) take the clamped form.
+template <int RULE>
+__device__ __forceinline__ bool block_is_plain(uint32_t amax_bits) {
+    return RULE == RULE_RCEIL && amax_bits - 0x04000000u < 0x7F800000u - 0x04000000u;
+}
+
+// Largest magnitude of two values and m; a NaN stays (v_maximum3_f32).
+__device__ __forceinline__ float amax3(float m, float a, float b) {
+    return __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, __builtin_fabsf(a)), __builtin_fabsf(b));
+}
+
 __device__ __forceinline__ uint32_t amax8_f32(const float (&x)[8]) {
-    uint32_t m = 0;
+    float m = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-    return m;
+    for (int e = 0; e < 8; e += 2) m = amax3(m, x[e], x[e + 1]);
+    return __float_as_uint(m) & 0x7FFFFFFFu;
 }
 
 // The MXFP8 row form of this lane's 8 consecutive values, its 32-value block being the 4 lanes of its quad.
 template <int RULE>
 __device__ __forceinline__ uint2 encode_row8(const float (&x)[8], uint32_t& byte) {
-    byte = mx_scale_byte_f32(quad_max(amax8_f32(x)), RULE);
+    const uint32_t m = quad_max(amax8_f32(x));
+    byte = mx_scale_byte_f32(m, RULE);
+    if (block_is_plain<RULE>(m)) {
+        const float s = scale_operand(byte);
+        return make_uint2(encode4_plain(x[0], x[1], x[2], x[3], s), encode4_plain(x[4], x[5], x[6], x[7], s));
+    }
     const float f = mx_inv_scale_f32(byte);
     return make_uint2(encode4(x[0], x[1], x[2], x[3], f), encode4(x[4], x[5], x[6], x[7], f));
 }
@@ -79,6 +106,53 @@ __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
     return v;
+}
+
+// ------------------------------------------------------------------ SwiGLU, bit for bit swiglu_f32's values
+// exp_fixed without its three special cases: x is first brought into [-105, 89], outside of which the fixed sequence
+// gives 0 and infinity by itself. (A NaN becomes a number here; the quotient g / (1 + e) is a NaN all the same.)
+__device__ __forceinline__ float exp_fixed_clamped(float x) {
+    x = __builtin_amdgcn_fmed3f(x, -105.0f, 89.0f);
+    const float k = __builtin_rintf(x * 1.44269504f);
+    float r = x - k * 0.693145751953125f;
+    r = r - k * 1.42860677e-06f;
+    float p = 1.0f / 720.0f;
+    p = p * r; p = p + 1.0f / 120.0f;
+    p = p * r; p = p + 1.0f / 24.0f;
+    p = p * r; p = p + 1.0f / 6.0f;
+    p = p * r; p = p + 0.5f;
+    p = p * r; p = p + 1.0f;
+    p = p * r; p = p + 1.0f;
+    return __builtin_ldexpf(p, (int)k);
+}
+
+// silu[e] = g / d and sig[e] = 1 / d, d = 1 + e^-g, both correctly rounded. Markstein's division: y, one Newton step
+// from the hardware's reciprocal, is the correctly rounded 1 / d (checked for every mantissa of d); q = g y is within an
+// ulp of the quotient, its remainder g - q d is exact, and q + remainder y rounds to the quotient. That holds while
+// nothing under- or overflows, which 2^-100 <= |g| <= 80 ensures; a wave that holds any other value (zeros, tiny or
+// huge ones, NaN) divides by the ordinary sequence: 6 operations instead of 20 for the pair.
+__device__ __forceinline__ void silu8(const float (&g)[8], float (&silu)[8], float (&sig)[8]) {
+    float hi = 0.0f, lo = 80.0f, d[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        d[e] = 1.0f + exp_fixed_clamped(-g[e]);
+        const float y0 = __builtin_amdgcn_rcpf(d[e]);
+        sig[e] = __builtin_fmaf(__builtin_fmaf(-d[e], y0, 1.0f), y0, y0);
+        const float q = g[e] * sig[e];
+        silu[e] = __builtin_fmaf(__builtin_fmaf(-q, d[e], g[e]), sig[e], q);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        hi = amax3(hi, g[e], g[e + 1]);
+        lo = __builtin_elementwise_minimum(__builtin_elementwise_minimum(lo, __builtin_fabsf(g[e])), __builtin_fabsf(g[e + 1]));
+    }
+    if (__any(!(hi <= 80.0f && lo >= 0x1p-100f))) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            silu[e] = g[e] / d[e];
+            sig[e] = 1.0f / d[e];
+        }
+    }
 }
 
 }  // namespace mxq

@@ -125,25 +125,35 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
     }
     __syncthreads();
     uint32_t d[32];
-    uint32_t m0 = 0, m1 = 0;
+    float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 32; ++r) {
+    for (int r = 0; r < 32; r += 2) {
         d[r] = lds[(32 * b + r) * (NT / 2) + p];
-        const float k = rs[32 * b + r];
-        m0 = max(m0, __float_as_uint((bf16_lo(d[r]) * k) * g0) & 0x7FFFFFFFu);
-        m1 = max(m1, __float_as_uint((bf16_hi(d[r]) * k) * g1) & 0x7FFFFFFFu);
+        d[r + 1] = lds[(32 * b + r + 1) * (NT / 2) + p];
+        const float2 k = *reinterpret_cast<const float2*>(&rs[32 * b + r]);
+        t0 = amax3(t0, (bf16_lo(d[r]) * k.x) * g0, (bf16_lo(d[r + 1]) * k.y) * g0);
+        t1 = amax3(t1, (bf16_hi(d[r]) * k.x) * g1, (bf16_hi(d[r + 1]) * k.y) * g1);
     }
+    const uint32_t m0 = __float_as_uint(t0) & 0x7FFFFFFFu, m1 = __float_as_uint(t1) & 0x7FFFFFFFu;
     const uint32_t b0 = mx_scale_byte_f32(m0, RULE), b1 = mx_scale_byte_f32(m1, RULE);
-    const float f0 = mx_inv_scale_f32(b0), f1 = mx_inv_scale_f32(b1);
     uint32_t o0[8], o1[8];
+    const bool plain = block_is_plain<RULE>(m0) && block_is_plain<RULE>(m1);
+    const float s0 = plain ? scale_operand(b0) : mx_inv_scale_f32(b0), s1 = plain ? scale_operand(b1) : mx_inv_scale_f32(b1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float4 k = *reinterpret_cast<const float4*>(&rs[32 * b + 4 * i]);
         const uint32_t* q = d + 4 * i;
-        o0[i] = encode4((bf16_lo(q[0]) * k.x) * g0, (bf16_lo(q[1]) * k.y) * g0, (bf16_lo(q[2]) * k.z) * g0,
-                        (bf16_lo(q[3]) * k.w) * g0, f0);
-        o1[i] = encode4((bf16_hi(q[0]) * k.x) * g1, (bf16_hi(q[1]) * k.y) * g1, (bf16_hi(q[2]) * k.z) * g1,
-                        (bf16_hi(q[3]) * k.w) * g1, f1);
+        const float y0 = (bf16_lo(q[0]) * k.x) * g0, y1 = (bf16_lo(q[1]) * k.y) * g0, y2 = (bf16_lo(q[2]) * k.z) * g0,
+                    y3 = (bf16_lo(q[3]) * k.w) * g0;
+        const float z0 = (bf16_hi(q[0]) * k.x) * g1, z1 = (bf16_hi(q[1]) * k.y) * g1, z2 = (bf16_hi(q[2]) * k.z) * g1,
+                    z3 = (bf16_hi(q[3]) * k.w) * g1;
+        if (plain) {
+            o0[i] = encode4_plain(y0, y1, y2, y3, s0);
+            o1[i] = encode4_plain(z0, z1, z2, z3, s1);
+        } else {
+            o0[i] = encode4(y0, y1, y2, y3, s0);
+            o1[i] = encode4(z0, z1, z2, z3, s1);
+        }
     }
     __syncthreads();                                             // every column pair has been read
     uint8_t* ob = reinterpret_cast<uint8_t*>(lds);               // 128 x 128 codes, then 128 x 4 scale bytes
