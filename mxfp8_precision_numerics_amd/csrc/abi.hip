@@ -500,7 +500,7 @@ mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_
                                          hipStream_t stream) {
     if (rule != MXQ_SCALE_RCEIL && rule != MXQ_SCALE_FLOOR) return MXQ_ERR_UNSUPPORTED;
     if (rows < 0 || F < 0 || F % 32 != 0) return MXQ_ERR_SHAPE;
-    if (F > (int64_t(1) << 24) || rows > (int64_t(1) << 38) / (F + 128)) return MXQ_ERR_SHAPE;   // the launch grid
+    if (F > (int64_t(1) << 22)) return MXQ_ERR_SHAPE;                            // 32-bit offsets within a tile
     if (rows == 0 || F == 0) return MXQ_OK;                                      // every pointer may be NULL
     if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr) ||
         (h_q_col == nullptr) != (h_s_col == nullptr))

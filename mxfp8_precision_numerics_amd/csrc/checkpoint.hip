@@ -50,10 +50,10 @@ __global__ __launch_bounds__(256) void swiglu_ck_fwd_kernel(const uint16_t* __re
 // 8 (tid % 16) .. + 7. The row orientation leaves from registers. d_gate, d_up and h go to three fp32 LDS tiles
 // (48 KiB), and after one barrier each of 3 x 128 threads encodes one column.
 //
-// silu and sigma by table: g^ is one of 256 codes times its block's scale, so for the CT_SCALES scales of ordinary
-// activations (blocks whose largest value lies between 0.007 and 448) a workgroup evaluates both once per code, 4096
-// pairs in 32 KiB of LDS, and reads them back in place of some 35 instructions a value. A wave that meets another scale
-// evaluates its values directly; both ways give the same bits.
+// silu and its derivative by table: g^ is one of 256 codes times its block's scale, so for the CT_SCALES scales of
+// ordinary activations (blocks whose largest value lies between 0.007 and 448) a workgroup evaluates both once per code,
+// 4096 pairs in 32 KiB of LDS, and reads them back in place of some 40 instructions a value. A wave that meets another
+// scale evaluates its values directly; both ways give the same bits.
 constexpr int CT_ROWS = 32, CT_COLS = 128, CT_THREADS = 512;
 constexpr int CT_SCALES = 16, CT_SCALE0 = 112;
 constexpr int64_t CT_GRID = 512;                               // two workgroups (2 x 80 KiB of LDS) per CU
@@ -63,8 +63,8 @@ struct CkBwdArgs {
     const uint16_t* dh;
     int64_t rows, F;
     uint8_t *q_row, *s_row, *q_col, *s_col, *h_q, *h_s;
-    int col_tiles, subs;        // tiles across; row tiles a workgroup takes one after the other (4 or 1)
-    int64_t ids;                // column tiles x groups of `subs` row tiles
+    uint32_t col_tiles, subs;   // tiles across; row tiles a workgroup takes one after the other (4 or 1)
+    uint32_t ids, share;        // column tiles x groups of `subs` row tiles; an XCD's share of them
 };
 
 __device__ __forceinline__ void put8(float* tile, int row, int ch, const float (&x)[8]) {
@@ -73,22 +73,43 @@ __device__ __forceinline__ void put8(float* tile, int row, int ch, const float (
     *reinterpret_cast<float4*>(d + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// silu = g / (1 + e^-g) and silu' = sigma (1 + g (1 - sigma)), sigma = 1 / (1 + e^-g); one rounding per operation.
+__device__ __forceinline__ void silu_and_slope8(const float (&g)[8], float (&silu)[8], float (&slope)[8]) {
+    silu8(g, silu, slope);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) slope[e] = slope[e] * (1.0f + g[e] * (1.0f - slope[e]));
+}
+
+// A thread's chunk of a tile, and the tile a workgroup is at. Offsets inside a group of row tiles fit 32 bits.
 struct CkChunk {
     uint2 g, u;
     uint4 d;
     uint32_t gs, us;
 };
+struct CkTile {
+    uint32_t id, sub, rows;     // group, row tile within the group, rows of the group
+    int64_t r0, c0;             // first row and column of the group
+};
 
-__device__ __forceinline__ CkChunk ck_load(const CkBwdArgs& a, int64_t gr, int64_t gc) {
-    CkChunk k{make_uint2(0u, 0u), make_uint2(0u, 0u), make_uint4(0u, 0u, 0u, 0u), 127u, 127u};
-    if (gc < a.F && gr < a.rows) {                               // whole quads: F % 32 == 0
-        const uint8_t* q = a.ck_q + gr * 2 * a.F + gc;
-        const uint8_t* s = a.ck_s + gr * (a.F / 16) + gc / 32;
-        k.g = ldnt8(q);
-        k.u = ldnt8(q + a.F);
-        k.d = ldnt16(a.dh + gr * a.F + gc);
-        k.gs = s[0];
-        k.us = s[a.F / 32];
+__device__ __forceinline__ void ck_group(const CkBwdArgs& a, CkTile& t) {
+    t.r0 = (int64_t)(t.id / a.col_tiles) * (a.subs * CT_ROWS);
+    t.c0 = (int64_t)(t.id % a.col_tiles) * CT_COLS;
+    t.sub = 0;
+    t.rows = (uint32_t)(a.rows - t.r0 < a.subs * CT_ROWS ? a.rows - t.r0 : a.subs * CT_ROWS);
+}
+
+__device__ __forceinline__ CkChunk ck_load(const CkBwdArgs& a, const CkTile& t, uint32_t rr, uint32_t cc) {
+    CkChunk k{make_uint2(0u, 0u), make_uint2(0u, 0u), make_uint4(0u, 0u, 0u, 0u), CT_SCALE0, 127u};
+    const uint32_t row = t.sub * CT_ROWS + rr, F = (uint32_t)a.F;
+    if (t.c0 + cc < F && row < t.rows) {                         // whole quads: F % 32 == 0
+        const uint8_t* q = a.ck_q + (t.r0 * 2 * F + t.c0);
+        const uint8_t* s = a.ck_s + (t.r0 * (F / 16) + t.c0 / 32);
+        const uint32_t qo = row * 2 * F + cc, so = row * (F / 16) + cc / 32;
+        k.g = ldnt8(q + qo);
+        k.u = ldnt8(q + F + qo);
+        k.d = ldnt16(a.dh + (t.r0 * F + t.c0) + (row * F + cc));
+        k.gs = s[so];
+        k.us = s[F / 32 + so];
     }
     return k;
 }
@@ -97,128 +118,142 @@ template <int RULE>
 __global__ __launch_bounds__(CT_THREADS, 4) void swiglu_ck_bwd_kernel(CkBwdArgs a) {
     __shared__ __attribute__((aligned(16))) float tile[3][CT_ROWS * CT_COLS];
     __shared__ __attribute__((aligned(16))) float2 table[CT_SCALES * 256];
-    const int tid = threadIdx.x, ch = tid & 15, rr = tid >> 4;
-    const int64_t F = a.F;
-    int64_t id = blockIdx.x;
-    int64_t c0 = id % a.col_tiles * CT_COLS, r0 = id / a.col_tiles * a.subs * CT_ROWS;
-    int sub = 0;
-    CkChunk next = ck_load(a, r0 + rr, c0 + 8 * ch);
+    const int tid = threadIdx.x;
+    const uint32_t cc = 8 * (tid & 15), rr = tid >> 4, F = (uint32_t)a.F;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform: the values below stay out of the lanes
+    const int which = wave >> 1, c = tid & (CT_COLS - 1);        // column phase: 0 d_gate, 1 d_up, 2 h
+    uint8_t* const qd = which == 2 ? a.h_q : which < 2 ? a.q_col : nullptr;
+    uint8_t* const sd = which == 2 ? a.h_s : a.s_col;
+    // Workgroups go to the 8 XCDs in turn: each XCD takes an eighth of the groups in order, so that the scale bytes of
+    // neighbouring tiles, a few to a 128-byte line, meet in one L2.
+    const uint32_t end = min(a.ids, (blockIdx.x % 8 + 1) * a.share);
+    CkTile t;
+    t.id = blockIdx.x % 8 * a.share + blockIdx.x / 8;
+    CkChunk next{};
+    if (t.id < end) {
+        ck_group(a, t);
+        next = ck_load(a, t, rr, cc);
+    }
     {
-        float g[8], silu[8], sig[8];                             // codes 8 (tid % 32) .. + 7 of scale tid / 32
+        float g[8], silu[8], slope[8];                           // codes 8 (tid % 32) .. + 7 of scale tid / 32
         const uint32_t q = 0x03020100u + 0x08080808u * (tid & 31);
         dequant8(make_uint2(q, q + 0x04040404u), e8m0_value(CT_SCALE0 + (tid >> 5)), g);
-        silu8(g, silu, sig);
+        silu_and_slope8(g, silu, slope);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) table[8 * tid + e] = make_float2(silu[e], sig[e]);
+        for (int e = 0; e < 8; ++e) table[8 * tid + e] = make_float2(silu[e], slope[e]);
     }
     __syncthreads();
-    uint4 held[3][2];                                            // this column's codes of the row tiles before, and
+    uint4 held[4][2];                                            // this column's codes of the group's row tiles, and
     uint32_t bytes = 0;                                          // their scale bytes
 #pragma unroll
-    for (int i = 0; i < 3; ++i) held[i][0] = held[i][1] = make_uint4(0u, 0u, 0u, 0u);
-    while (id < a.ids) {
+    for (int i = 0; i < 4; ++i) held[i][0] = held[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    while (t.id < end) {
         const CkChunk k = next;
-        const int64_t gr = r0 + rr, gc = c0 + 8 * ch, cr0 = r0, cc0 = c0;
-        const int csub = sub;
-        const bool ok = gc < F && gr < a.rows;
-        r0 += CT_ROWS;
-        if (++sub == a.subs || r0 >= a.rows) {                   // the next tile: below this one, or another group's
-            sub = 0;
-            id += gridDim.x;
-            c0 = id % a.col_tiles * CT_COLS;
-            r0 = id / a.col_tiles * a.subs * CT_ROWS;
+        const CkTile now = t;
+        const bool last = (now.sub + 1) * CT_ROWS >= now.rows;   // the group's last row tile
+        if (last) {
+            t.id += gridDim.x / 8;
+            if (t.id < end) ck_group(a, t);
+        } else {
+            ++t.sub;
         }
-        if (id < a.ids) next = ck_load(a, r0 + rr, c0 + 8 * ch);
-        {
-            float g[8], u[8], d[8], silu[8], sig[8], xg[8], xu[8], xh[8];
-            dequant8(k.g, e8m0_value(k.gs), g);
-            dequant8(k.u, e8m0_value(k.us), u);
-            unpack8(k.d, d);
-            if (__any(k.gs - CT_SCALE0 >= (uint32_t)CT_SCALES)) {
-                silu8(g, silu, sig);
-            } else {
-                const float2* t = table + 256 * (k.gs - CT_SCALE0);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 v = t[((e < 4 ? k.g.x : k.g.y) >> (8 * (e & 3))) & 255u];
-                    silu[e] = v.x;
-                    sig[e] = v.y;
-                }
-            }
-            // silu = g / (1 + e^-g), sigma = 1 / (1 + e^-g), silu' = sigma (1 + g (1 - sigma))
+        if (t.id < end) next = ck_load(a, t, rr, cc);
+        const uint32_t row = now.sub * CT_ROWS + rr;
+        float silu[8], slope[8], x[8], v[8];
+        if (__any(k.gs - CT_SCALE0 >= (uint32_t)CT_SCALES)) {
+            dequant8(k.g, e8m0_value(k.gs), v);
+            silu_and_slope8(v, silu, slope);
+        } else {
+            const float2* e0 = table + 256 * (k.gs - CT_SCALE0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                xg[e] = (d[e] * u[e]) * (sig[e] * (1.0f + g[e] * (1.0f - sig[e])));
-                xu[e] = d[e] * silu[e];
-                xh[e] = silu[e] * u[e];
+                const float2 w = e0[((e < 4 ? k.g.x : k.g.y) >> (8 * (e & 3))) & 255u];
+                silu[e] = w.x;
+                slope[e] = w.y;
             }
-            if (a.q_row && ok) {
-                uint32_t bg, bu;
-                uint8_t* q = a.q_row + gr * 2 * F + gc;
-                stnt8(q, encode_row8<RULE>(xg, bg));
-                stnt8(q + F, encode_row8<RULE>(xu, bu));
-                if ((ch & 3) == 0) {
-                    uint8_t* s = a.s_row + gr * (F / 16) + gc / 32;
-                    s[0] = (uint8_t)bg;
-                    s[F / 32] = (uint8_t)bu;
-                }
-            }
-            if (a.q_col || a.h_q) {
-                put8(tile[0], rr, ch, xg);
-                put8(tile[1], rr, ch, xu);
-                put8(tile[2], rr, ch, xh);
-            }
+        }
+        const bool row_ok = a.q_row && now.c0 + cc < F && row < now.rows;
+        uint8_t* qr = a.q_row + (now.r0 * 2 * F + now.c0);
+        uint8_t* sr = a.s_row + (now.r0 * (F / 16) + now.c0 / 32);
+        const uint32_t qo = row * 2 * F + cc, so = row * (F / 16) + cc / 32;
+        uint32_t byte;
+        float d[8];
+        dequant8(k.u, e8m0_value(k.us), v);
+        unpack8(k.d, d);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = silu[e] * v[e];       // h
+        put8(tile[2], rr, cc / 8, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = d[e] * silu[e];       // d_up
+        put8(tile[1], rr, cc / 8, x);
+        if (row_ok) {
+            stnt8(qr + F + qo, encode_row8<RULE>(x, byte));
+            if ((tid & 3) == 0) sr[F / 32 + so] = (uint8_t)byte;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = (d[e] * v[e]) * slope[e];   // d_gate
+        put8(tile[0], rr, cc / 8, x);
+        if (row_ok) {
+            stnt8(qr + qo, encode_row8<RULE>(x, byte));
+            if ((tid & 3) == 0) sr[so] = (uint8_t)byte;
         }
         if (!a.q_col && !a.h_q) continue;
         __syncthreads();
-        const int which = tid >> 7, c = tid & (CT_COLS - 1);     // 0: d_gate, 1: d_up, 2: h
-        if (which < 3 && cc0 + c < F && (which < 2 ? a.q_col : a.h_q)) {
-            float d[32], top = 0.0f;
+        if (qd && now.c0 + c < F) {
+            float y[32], top = 0.0f;
 #pragma unroll
             for (int r = 0; r < 32; r += 2) {
-                d[r] = tile[which][r * CT_COLS + c];
-                d[r + 1] = tile[which][(r + 1) * CT_COLS + c];
-                top = amax3(top, d[r], d[r + 1]);
+                y[r] = tile[which][r * CT_COLS + c];
+                y[r + 1] = tile[which][(r + 1) * CT_COLS + c];
+                top = amax3(top, y[r], y[r + 1]);
             }
             const uint32_t m = __float_as_uint(top) & 0x7FFFFFFFu;
-            const uint32_t byte = mx_scale_byte_f32(m, RULE);
+            const uint32_t b = mx_scale_byte_f32(m, RULE);
             uint32_t o[8];
             if (block_is_plain<RULE>(m)) {
-                const float s = scale_operand(byte);
+                const float s = scale_operand(b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = encode4_plain(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3], s);
+                for (int i = 0; i < 8; ++i) o[i] = encode4_plain(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3], s);
             } else {
-                const float f = mx_inv_scale_f32(byte);
+                const float f = mx_inv_scale_f32(b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = encode4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3], f);
+                for (int i = 0; i < 8; ++i) o[i] = encode4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3], f);
             }
-            // Four row tiles make a 128-byte line of the column: it is written at once, from the registers, so that the
-            // caches need not hold thousands of part-written lines.
             const uint4 o0 = make_uint4(o[0], o[1], o[2], o[3]), o1 = make_uint4(o[4], o[5], o[6], o[7]);
-            bytes = (csub ? bytes : 0u) | byte << (8 * csub);
-            if (csub == 0) { held[0][0] = o0; held[0][1] = o1; }
-            if (csub == 1) { held[1][0] = o0; held[1][1] = o1; }
-            if (csub == 2) { held[2][0] = o0; held[2][1] = o1; }
-            if (sub == 0) {                                      // the group's last row tile
-                const int64_t col = cc0 + c + (which == 1 ? F : 0), g0 = cr0 - csub * CT_ROWS;
-                uint8_t* qd = a.q_col;
-                uint8_t* sd = a.s_col;
-                if (which == 2) { qd = a.h_q; sd = a.h_s; }
-                uint4* q = reinterpret_cast<uint4*>(qd + col * a.rows + g0);          // rows % 32 == 0
-                sd += col * (a.rows / 32) + g0 / CT_ROWS;
+            bytes = (now.sub ? bytes : 0u) | b << (8 * now.sub);
+            if (now.sub == 0) { held[0][0] = o0; held[0][1] = o1; }
+            if (now.sub == 1) { held[1][0] = o0; held[1][1] = o1; }
+            if (now.sub == 2) { held[2][0] = o0; held[2][1] = o1; }
+            if (now.sub == 3) { held[3][0] = o0; held[3][1] = o1; }
+        }
+        __syncthreads();
+        if (!last) continue;
+        // The group's codes: up to 128 bytes a column, one column per thread, through LDS (the tiles' memory) to 8 lanes
+        // a column, so that memory gets whole 128-byte lines. Piece k of column c sits at k ^ (c % 8).
+        uint4* stage = reinterpret_cast<uint4*>(&tile[0][0]);
+        if (which < 3) {
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (csub > i) {
-                        q[2 * i] = held[i][0];
-                        q[2 * i + 1] = held[i][1];
-                    }
-                q[2 * csub] = o0;
-                q[2 * csub + 1] = o1;
-                if (csub == 3 && a.rows % 128 == 0) {
-                    *reinterpret_cast<uint32_t*>(sd) = bytes;
-                } else {
-                    for (int i = 0; i <= csub; ++i) sd[i] = (uint8_t)(bytes >> (8 * i));
-                }
+            for (int i = 0; i < 8; ++i) stage[8 * tid + (i ^ (c & 7))] = held[i >> 1][i & 1];
+        }
+        if (qd && now.c0 + c < F) {
+            uint8_t* s = sd + (now.c0 + c + (which == 1 ? F : 0)) * (a.rows / 32) + now.r0 / 32;
+            if (now.rows == 128 && a.rows % 128 == 0) {
+                *reinterpret_cast<uint32_t*>(s) = bytes;
+            } else {
+                for (uint32_t i = 0; i <= now.sub; ++i) s[i] = (uint8_t)(bytes >> (8 * i));
+            }
+        }
+        __syncthreads();
+        const uint32_t piece = tid & 7;
+        if (16 * piece < now.rows) {                             // rows % 32 == 0
+#pragma unroll
+            for (int i = 0; i < 6; ++i) {
+                const uint32_t at = 64 * i + (tid >> 3);         // 0 .. 383: output at / 128, column at % 128
+                const int out = (64 * i + 8 * wave) >> 7;
+                uint8_t* q = out == 2 ? a.h_q : a.q_col;
+                if (q && now.c0 + (at & 127) < F)
+                    *reinterpret_cast<uint4*>(q + (now.c0 + (at & 127) + (out == 1 ? F : 0)) * a.rows + now.r0 + 16 * piece) =
+                        stage[8 * at + (piece ^ (at & 7))];
             }
         }
         __syncthreads();
@@ -242,9 +277,10 @@ hipError_t launch_swiglu_bwd_checkpoint(const uint8_t* ck_q, const uint8_t* ck_s
     const int64_t col_tiles = (F + CT_COLS - 1) / CT_COLS, row_tiles = (rows + CT_ROWS - 1) / CT_ROWS;
     // whole lines of the column orientation where that still fills the chip, else one row tile a workgroup
     const int64_t subs = col_tiles * ((row_tiles + 3) / 4) >= CT_GRID ? 4 : 1;
-    const CkBwdArgs a{ck_q, ck_s, dh, rows, F, q_row, s_row, q_col, s_col, h_q, h_s, (int)col_tiles, (int)subs,
-                      col_tiles * ((row_tiles + subs - 1) / subs)};
-    const dim3 grid((unsigned)(a.ids < CT_GRID ? a.ids : CT_GRID));
+    const int64_t ids = col_tiles * ((row_tiles + subs - 1) / subs), share = (ids + 7) / 8;
+    const CkBwdArgs a{ck_q, ck_s, dh, rows, F, q_row, s_row, q_col, s_col, h_q, h_s, (uint32_t)col_tiles,
+                      (uint32_t)subs, (uint32_t)ids, (uint32_t)share};
+    const dim3 grid((unsigned)(8 * (share < CT_GRID / 8 ? share : CT_GRID / 8)));
     if (rule == RULE_FLOOR) hipLaunchKernelGGL(swiglu_ck_bwd_kernel<RULE_FLOOR>, grid, dim3(CT_THREADS), 0, stream, a);
     else hipLaunchKernelGGL(swiglu_ck_bwd_kernel<RULE_RCEIL>, grid, dim3(CT_THREADS), 0, stream, a);
     return hipGetLastError();
