@@ -252,8 +252,8 @@ __global__ __launch_bounds__(CT_THREADS, 4) void swiglu_ck_bwd_kernel(CkBwdArgs 
                 const int out = (64 * i + 8 * wave) >> 7;
                 uint8_t* q = out == 2 ? a.h_q : a.q_col;
                 if (q && now.c0 + (at & 127) < F)
-                    *reinterpret_cast<uint4*>(q + (now.c0 + (at & 127) + (out == 1 ? F : 0)) * a.rows + now.r0 + 16 * piece) =
-                        stage[8 * at + (piece ^ (at & 7))];
+                    stnt16(q + (now.c0 + (at & 127) + (out == 1 ? F : 0)) * a.rows + now.r0 + 16 * piece,
+                           stage[8 * at + (piece ^ (at & 7))]);
             }
         }
         __syncthreads();

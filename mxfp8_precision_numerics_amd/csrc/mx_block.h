@@ -1,6 +1,8 @@
 // Device helpers shared by the block kernels (norm.hip, checkpoint.hip, moe_few.hip): 8 values of one row as packed
 // bf16, fp32 or MXFP8, and the sums across a wave. Internal; not part of the C ABI.
 #pragma once
+#include <type_traits>
+
 #include "mxq_device.h"
 
 namespace mxq {
@@ -101,11 +103,27 @@ __device__ __forceinline__ uint2 encode_row8_bf16(uint4 v, uint32_t& byte) {
     return make_uint2(lo, hi);
 }
 
-// Sum over the 64 lanes of a wave; every lane gets the same value (each step adds the same two numbers on both sides).
+// Joins a value over the 64 lanes of a wave by lane permutations within 16-lane rows and swaps of rows and halves (no
+// LDS); every lane gets the same result, as each step joins the same two values on both sides.
+template <class Op>
+__device__ __forceinline__ float wave_join(float v, Op op) {
+    auto dpp = [](float x, auto ctrl) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(x), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    v = op(v, dpp(v, std::integral_constant<int, 0xB1>{}));      // lanes i ^ 1
+    v = op(v, dpp(v, std::integral_constant<int, 0x4E>{}));      // lanes i ^ 2
+    v = op(v, dpp(v, std::integral_constant<int, 0x141>{}));     // the other quad of 8 (row_half_mirror)
+    v = op(v, dpp(v, std::integral_constant<int, 0x140>{}));     // the other 8 of 16 (row_mirror)
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = op(__uint_as_float((uint32_t)r[0]), __uint_as_float((uint32_t)r[1]));
+    const auto h = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return op(__uint_as_float((uint32_t)h[0]), __uint_as_float((uint32_t)h[1]));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-    return v;
+    return wave_join(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float wave_max(float v) {
+    return wave_join(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
 }
 
 // ------------------------------------------------------------------ SwiGLU, bit for bit swiglu_f32's values
