@@ -77,14 +77,13 @@ hipError_t launch_adam_delayed(float* master, const uint16_t* grad, uint8_t* m_q
                                uint16_t* w, int64_t n, const AdamConsts& k, float* hist, int32_t* pos, int H,
                                float* consts, uint32_t* amax_word, hipStream_t stream);
 
-// RMSNorm (norm.hip). sum may be x or res; the partial rows of dgamma number rmsnorm_backward_parts(rows).
+// RMSNorm (norm.hip). sum may be x or res; the backward writes at most kNormBwdParts partial rows of dgamma.
 constexpr int64_t kNormMaxCols = 32768;
 constexpr int64_t kNormBwdParts = 512;
 hipError_t launch_rmsnorm_mx_quantize(const uint16_t* x, const uint16_t* res, const float* gamma, int64_t rows,
                                       int64_t cols, float eps, uint16_t* sum, float* rstd, uint8_t* q_row,
                                       uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, uint8_t* ck_q, uint8_t* ck_s,
                                       int rule, hipStream_t stream);
-int rmsnorm_backward_parts(int64_t rows);
 hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* dres, const uint8_t* ck_q, const uint8_t* ck_s,
                                    const float* rstd, const float* gamma, int64_t rows, int64_t cols, uint16_t* dx,
                                    float* dgamma, int accumulate, float* partial, hipStream_t stream);

@@ -182,105 +182,179 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
 }
 
 // ---------------------------------------------------------------------------------------- backward
-// A workgroup walks rows blockIdx.x, blockIdx.x + gridDim.x, ... with the row split over W waves as in the forward;
-// each lane keeps gamma and its columns' dgamma sums in registers over all its rows and writes one partial row of
-// dgamma at the end. norm_dgamma_kernel adds the partial rows in a fixed order, so the result does not depend on timing.
-template <int W, int NCH>
-__global__ __launch_bounds__(64 * W) void norm_bwd_kernel(const uint16_t* dy, const uint16_t* dres, const uint8_t* ck_q,
-                                                        const uint8_t* ck_s, const float* rstd, const float* gamma,
-                                                        int64_t rows, int64_t cols, uint16_t* dx, float* partial) {
-    __shared__ float part[2][W];
-    const int t = threadIdx.x;
-    const int chunks = (int)(cols / 8);
-    float g[NCH][8], acc[NCH][8];
+// W waves share a row as in the forward; W < 8 packs R = 8 / W rows into a workgroup. A workgroup walks its rows in steps
+// of the whole grid. The next rows' loads are issued before these are reduced; xh is formed twice from the codes (for the
+// sums, then for dx) rather than kept. Each lane keeps gamma and its columns' dgamma sums in registers over all its rows;
+// the workgroup writes one partial row of dgamma at the end, and norm_dgamma_kernel adds the partial rows in a fixed
+// order, so the result does not depend on timing. Rows too wide for that in registers (W = 16: 128 of them a lane) read
+// gamma again for each row and load nothing ahead.
+template <int NCH>
+struct BwdRow {
+    uint4 dy[NCH], dr[NCH];
+    uint2 q[NCH];
+    uint32_t s[NCH];
+    float rstd;
+};
+
+struct BwdArgs {
+    const uint16_t *dy, *dres;
+    const uint8_t *ck_q, *ck_s;
+    const float *rstd, *gamma;
+    int64_t rows;
+    uint32_t cols;
+    uint16_t* dx;
+    float* partial;             // NULL: no dgamma
+};
+
+template <int W, int NCH, bool RES>
+__device__ __forceinline__ void load_row(BwdRow<NCH>& x, const BwdArgs& a, int64_t row, uint32_t t) {
+    const uint32_t cols = a.cols;
+    const bool row_ok = row < a.rows;
+    const uint16_t* p = a.dy + row * cols;
+    const uint16_t* d = a.dres + row * cols;
+    const uint8_t* q = a.ck_q + row * cols;
+    const uint8_t* s = a.ck_s + row * (cols / 32);
+    x.rstd = row_ok ? a.rstd[row] : 0.0f;
 #pragma unroll
     for (int j = 0; j < NCH; ++j) {
-        const int ch = t + 64 * W * j;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            acc[j][e] = 0.0f;
-            g[j][e] = ch < chunks ? gamma[8 * ch + e] : 0.0f;
-        }
-    }
-    int par = 0;
-    for (int64_t row = blockIdx.x; row < rows; row += gridDim.x, par ^= 1) {
-        const float rs = rstd[row];
-        float xh[NCH][8];
-        uint4 d[NCH];
-        float dot = 0.0f;
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            const int ch = t + 64 * W * j;
-            if (ch < chunks) {
-                const int64_t at = row * cols + 8 * ch;
-                d[j] = ldnt16(dy + at);
-                dequant8(ldnt8(ck_q + at), e8m0_value(ck_s[row * (cols / 32) + ch / 4]), xh[j]);
-            } else {
-                d[j] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) xh[j][e] = 0.0f;
-            }
-            float v[8];
-            unpack8(d[j], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                xh[j][e] = xh[j][e] * rs;
-                acc[j][e] += v[e] * xh[j][e];
-                dot += (v[e] * g[j][e]) * xh[j][e];
-            }
-        }
-        dot = wave_sum(dot);
-        if constexpr (W > 1) {
-            if ((t & 63) == 0) part[par][t >> 6] = dot;          // two buffers: one barrier per row suffices
-            __syncthreads();
-            dot = part[par][0];
-#pragma unroll
-            for (int w = 1; w < W; ++w) dot += part[par][w];
-        }
-        const float m = dot / (float)cols;
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            const int ch = t + 64 * W * j;
-            if (ch >= chunks) continue;
-            const int64_t at = row * cols + 8 * ch;
-            float v[8], r[8];
-            unpack8(d[j], v);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = rs * (v[e] * g[j][e] - xh[j][e] * m);
-            if (dres) {
-                unpack8(ldnt16(dres + at), r);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = r[e] + v[e];
-            }
-            stnt16(dx + at, pack8(v));
-        }
-    }
-    if (partial) {
-#pragma unroll
-        for (int j = 0; j < NCH; ++j) {
-            const int ch = t + 64 * W * j;
-            if (ch >= chunks) continue;
-            float* o = partial + (int64_t)blockIdx.x * cols + 8 * ch;
-            *reinterpret_cast<float4*>(o) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-            *reinterpret_cast<float4*>(o + 4) = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+        const uint32_t ch = t + 64 * W * j;
+        x.dy[j] = x.dr[j] = make_uint4(0u, 0u, 0u, 0u);
+        x.q[j] = make_uint2(0u, 0u);
+        x.s[j] = 127u;
+        if (row_ok && ch < cols / 8) {
+            x.dy[j] = ldnt16(p + 8 * ch);
+            x.q[j] = ldnt8(q + 8 * ch);
+            x.s[j] = s[ch / 4];
+            if constexpr (RES) x.dr[j] = ldnt16(d + 8 * ch);
         }
     }
 }
 
-// dgamma[c] = (accumulate ? dgamma[c] : 0) + sum of the partial rows: 32 columns x 8 slices of the rows per workgroup.
+__device__ __forceinline__ void load_gamma(const float* gamma, uint32_t ch, uint32_t chunks, float (&g)[8]) {
+    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+    if (ch < chunks) {
+        u = *reinterpret_cast<const float4*>(gamma + 8 * ch);
+        v = *reinterpret_cast<const float4*>(gamma + 8 * ch + 4);
+    }
+    g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w; g[4] = v.x; g[5] = v.y; g[6] = v.z; g[7] = v.w;
+}
+
+template <int W, int NCH, bool RES>
+__global__ __launch_bounds__(W < 8 ? 512 : 64 * W) void norm_bwd_kernel(BwdArgs a) {
+    constexpr int R = W < 8 ? 8 / W : 1;
+    constexpr bool AHEAD = W < 16;
+    static_assert(R == 1 || NCH == 1, "rows that share a workgroup have one chunk a lane");
+    __shared__ float part[2][R * W];
+    __shared__ __attribute__((aligned(16))) float comb[R > 1 ? 512 * 8 : 4];
+    const uint32_t t = threadIdx.x % (64 * W), sub = threadIdx.x / (64 * W), cols = a.cols, chunks = cols / 8;
+    const int64_t step = (int64_t)gridDim.x * R;
+    float g[NCH][8], acc[NCH][8];
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        if constexpr (AHEAD) load_gamma(a.gamma, t + 64 * W * j, chunks, g[j]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
+    }
+    BwdRow<NCH> next;
+    int64_t base = (int64_t)blockIdx.x * R;
+    if constexpr (AHEAD) load_row<W, NCH, RES>(next, a, base + sub, t);
+    int par = 0;
+    for (; base < a.rows; base += step, par ^= 1) {
+        const int64_t row = base + sub;
+        BwdRow<NCH> x;
+        if constexpr (AHEAD) {
+            x = next;
+            load_row<W, NCH, RES>(next, a, row + step, t);
+        } else {
+            load_row<W, NCH, RES>(x, a, row, t);
+        }
+        const float rs = x.rstd;
+        float dot = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            float v[8], xh[8];
+            if constexpr (!AHEAD) load_gamma(a.gamma, t + 64 * W * j, chunks, g[j]);
+            unpack8(x.dy[j], v);
+            dequant8(x.q[j], e8m0_value(x.s[j]), xh);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                xh[e] = xh[e] * rs;
+                acc[j][e] += v[e] * xh[e];
+                dot += (v[e] * g[j][e]) * xh[e];
+            }
+        }
+        dot = wave_sum(dot);
+        if constexpr (W > 1) {
+            if ((threadIdx.x & 63) == 0) part[par][threadIdx.x >> 6] = dot;      // two buffers: one barrier a row
+            __syncthreads();
+            dot = part[par][sub * W];
+#pragma unroll
+            for (int w = 1; w < W; ++w) dot += part[par][sub * W + w];
+        }
+        const float m = dot / (float)cols;
+        uint16_t* o = a.dx + row * cols;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const uint32_t ch = t + 64 * W * j;
+            if (!(row < a.rows && ch < chunks)) continue;
+            float v[8], xh[8];
+            if constexpr (!AHEAD) load_gamma(a.gamma, ch, chunks, g[j]);
+            unpack8(x.dy[j], v);
+            dequant8(x.q[j], e8m0_value(x.s[j]), xh);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = rs * (v[e] * g[j][e] - (xh[e] * rs) * m);
+            if constexpr (RES) {
+                float r[8];
+                unpack8(x.dr[j], r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = r[e] + v[e];
+            }
+            stnt16(o + 8 * ch, pack8(v));
+        }
+    }
+    if (!a.partial) return;
+    if constexpr (R > 1) {                                       // the rows' sums, added in order
+        float* c = comb + 8 * threadIdx.x;
+        *reinterpret_cast<float4*>(c) = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+        *reinterpret_cast<float4*>(c + 4) = make_float4(acc[0][4], acc[0][5], acc[0][6], acc[0][7]);
+        __syncthreads();
+        if (sub != 0) return;
+#pragma unroll
+        for (int q = 1; q < R; ++q)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[0][e] += comb[8 * (t + 64 * W * q) + e];
+    }
+#pragma unroll
+    for (int j = 0; j < NCH; ++j) {
+        const uint32_t ch = t + 64 * W * j;
+        if (ch >= chunks) continue;
+        float* o = a.partial + (int64_t)blockIdx.x * cols + 8 * ch;
+        *reinterpret_cast<float4*>(o) = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+        *reinterpret_cast<float4*>(o + 4) = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+    }
+}
+
+// dgamma[c] = (accumulate ? dgamma[c] : 0) + sum of the partial rows. A workgroup has 32 columns, 4 to a lane, and 32
+// slices of the rows: slice k adds rows k, k + 32, ..., eight loads in flight, and the slices are added in order.
 __global__ __launch_bounds__(256) void norm_dgamma_kernel(const float* partial, int parts, int64_t cols, float* dgamma,
                                                          int accumulate) {
-    __shared__ float s[8][32];
-    const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
-    const int64_t col = (int64_t)blockIdx.x * 32 + c;            // cols % 32 == 0
-    float v = 0.0f;
-    for (int p = k; p < parts; p += 8) v += partial[(int64_t)p * cols + col];
-    s[k][c] = v;
+    __shared__ __attribute__((aligned(16))) float s[32][32];
+    const int c = 4 * (threadIdx.x & 7), k = threadIdx.x >> 3;
+    const float* p = partial + (int64_t)blockIdx.x * 32 + c;     // cols % 32 == 0
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+    for (int r = k; r < parts; r += 32) {
+        const float4 x = *reinterpret_cast<const float4*>(p + (int64_t)r * cols);
+        v.x += x.x; v.y += x.y; v.z += x.z; v.w += x.w;
+    }
+    *reinterpret_cast<float4*>(&s[k][c]) = v;
     __syncthreads();
-    if (k == 0) {
+    if (threadIdx.x < 32) {
+        float y = s[0][threadIdx.x];
 #pragma unroll
-        for (int q = 1; q < 8; ++q) v += s[q][c];
-        dgamma[col] = accumulate ? dgamma[col] + v : v;
+        for (int q = 1; q < 32; ++q) y += s[q][threadIdx.x];
+        float* d = dgamma + (int64_t)blockIdx.x * 32 + threadIdx.x;
+        *d = accumulate ? *d + y : y;
     }
 }
 
@@ -318,27 +392,33 @@ hipError_t launch_rmsnorm_mx_quantize(const uint16_t* x, const uint16_t* res, co
     return hipGetLastError();
 }
 
-int rmsnorm_backward_parts(int64_t rows) { return (int)(rows < kNormBwdParts ? rows : kNormBwdParts); }
+// Workgroups: two to a CU while their registers allow it (W < 12), else one.
+template <int W, int NCH>
+static int run_bwd(const BwdArgs& a, hipStream_t stream) {
+    constexpr int R = W < 8 ? 8 / W : 1;
+    constexpr int64_t MOST = W < 12 ? kNormBwdParts : kNormBwdParts / 2;
+    const int64_t groups = (a.rows + R - 1) / R;
+    const int parts = (int)(groups < MOST ? groups : MOST);
+    if (a.dres) hipLaunchKernelGGL((norm_bwd_kernel<W, NCH, true>), dim3(parts), dim3(64 * W * R), 0, stream, a);
+    else hipLaunchKernelGGL((norm_bwd_kernel<W, NCH, false>), dim3(parts), dim3(64 * W * R), 0, stream, a);
+    return parts;
+}
 
 hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* dres, const uint8_t* ck_q, const uint8_t* ck_s,
                                    const float* rstd, const float* gamma, int64_t rows, int64_t cols, uint16_t* dx,
                                    float* dgamma, int accumulate, float* partial, hipStream_t stream) {
-    const int parts = rmsnorm_backward_parts(rows);
-    float* part = dgamma ? partial : nullptr;
-#define MXQ_NORM_BWD(W, N)                                                                                          \
-    hipLaunchKernelGGL((norm_bwd_kernel<W, N>), dim3((unsigned)parts), dim3(64 * W), 0, stream, dy, dres, ck_q, ck_s, \
-                       rstd, gamma, rows, cols, dx, part)
+    const BwdArgs a{dy, dres, ck_q, ck_s, rstd, gamma, rows, (uint32_t)cols, dx, dgamma ? partial : nullptr};
+    int parts = 0;
     if (rows > 0) {
-        if (cols <= 512) MXQ_NORM_BWD(1, 1);
-        else if (cols <= 1024) MXQ_NORM_BWD(2, 1);
-        else if (cols <= 2048) MXQ_NORM_BWD(4, 1);
-        else if (cols <= 4096) MXQ_NORM_BWD(4, 2);
-        else if (cols <= 8192) MXQ_NORM_BWD(8, 2);
-        else if (cols <= 12288) MXQ_NORM_BWD(8, 3);
-        else if (cols <= 16384) MXQ_NORM_BWD(16, 2);
-        else MXQ_NORM_BWD(16, 4);
+        if (cols <= 512) parts = run_bwd<1, 1>(a, stream);
+        else if (cols <= 1024) parts = run_bwd<2, 1>(a, stream);
+        else if (cols <= 2048) parts = run_bwd<4, 1>(a, stream);
+        else if (cols <= 4096) parts = run_bwd<8, 1>(a, stream);
+        else if (cols <= 8192) parts = run_bwd<8, 2>(a, stream);
+        else if (cols <= 12288) parts = run_bwd<12, 2>(a, stream);
+        else if (cols <= 16384) parts = run_bwd<16, 2>(a, stream);
+        else parts = run_bwd<16, 4>(a, stream);
     }
-#undef MXQ_NORM_BWD
     if (dgamma)
         hipLaunchKernelGGL(norm_dgamma_kernel, dim3((unsigned)(cols / 32)), dim3(256), 0, stream, partial, parts, cols,
                            dgamma, accumulate);
