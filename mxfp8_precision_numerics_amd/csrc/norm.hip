@@ -186,7 +186,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
 // of the whole grid. The next rows' loads are issued before these are reduced; xh is formed twice from the codes (for the
 // sums, then for dx) rather than kept. Each lane keeps gamma and its columns' dgamma sums in registers over all its rows;
 // the workgroup writes one partial row of dgamma at the end, and norm_dgamma_kernel adds the partial rows in a fixed
-// order, so the result does not depend on timing. Rows too wide for that in registers (W = 16: 128 of them a lane) read
+// order, so the result does not depend on timing. Rows too wide for that in the registers of 16 waves (two chunks a lane) read
 // gamma again for each row and load nothing ahead.
 template <int NCH>
 struct BwdRow {
@@ -242,7 +242,7 @@ __device__ __forceinline__ void load_gamma(const float* gamma, uint32_t ch, uint
 template <int W, int NCH, bool RES>
 __global__ __launch_bounds__(W < 8 ? 512 : 64 * W) void norm_bwd_kernel(BwdArgs a) {
     constexpr int R = W < 8 ? 8 / W : 1;
-    constexpr bool AHEAD = W < 16;
+    constexpr bool AHEAD = W < 16 || NCH == 1;
     static_assert(R == 1 || NCH == 1, "rows that share a workgroup have one chunk a lane");
     __shared__ float part[2][R * W];
     __shared__ __attribute__((aligned(16))) float comb[R > 1 ? 512 * 8 : 4];
@@ -414,7 +414,7 @@ hipError_t launch_rmsnorm_backward(const uint16_t* dy, const uint16_t* dres, con
         else if (cols <= 1024) parts = run_bwd<2, 1>(a, stream);
         else if (cols <= 2048) parts = run_bwd<4, 1>(a, stream);
         else if (cols <= 4096) parts = run_bwd<8, 1>(a, stream);
-        else if (cols <= 8192) parts = run_bwd<8, 2>(a, stream);
+        else if (cols <= 8192) parts = run_bwd<16, 1>(a, stream);
         else if (cols <= 12288) parts = run_bwd<12, 2>(a, stream);
         else if (cols <= 16384) parts = run_bwd<16, 2>(a, stream);
         else parts = run_bwd<16, 4>(a, stream);
