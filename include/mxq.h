@@ -401,7 +401,7 @@ mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_
                                          hipStream_t stream);
 
 /*
- * The routed experts of a few tokens (1 <= tokens <= 64; 0 is empty) in two launches, with no dispatch and no padding
+ * The routed experts of a few tokens (1 <= tokens <= 64; 0 is empty) in two or three launches, with no dispatch and no padding
  * to 32 rows an expert: for decoding and for small evaluation batches. Per token t:
  *   the topk largest logits (fp32[tokens][experts]) choose its experts, equal logits by the lower index; p = the softmax
  *   of the chosen logits (normalize != 0) or their share of the softmax over all logits (normalize == 0);
@@ -413,7 +413,7 @@ mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_
  * A logit of -inf is never chosen (a token with fewer than topk finite logits uses those; one with none gets a row of
  * zeros); a NaN or +inf among a token's logits makes its row NaN. Results do not depend on timing.
  * Requires experts <= 1024, 1 <= topk <= min(experts, 32), D and F positive multiples of 32 up to 2^20. workspace:
- * moe_mx_few_tokens_workspace_bytes(tokens, experts, topk, F) bytes, clobbered; that call returns 0 for sizes out of
+ * moe_mx_few_tokens_workspace_bytes(tokens, experts, topk, D, F) bytes, clobbered; that call returns 0 for sizes out of
  * range.
  */
 mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float* logits, int64_t tokens,
@@ -421,7 +421,7 @@ mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float
                              const uint8_t* w_up_s, const uint8_t* w_down_q, const uint8_t* w_down_s, int64_t D,
                              int64_t F, uint16_t* y_bf16, void* workspace, size_t workspace_bytes,
                              hipStream_t stream);
-size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t F);
+size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t D, int64_t F);
 
 /* Adam hyper-parameters, passed by HOST pointer. step is the 1-based step count t (MXQ_ERR_SHAPE if below 1);
  * beta1 and beta2 lie in [0, 1) (MXQ_ERR_UNSUPPORTED otherwise, NaN included). Every Adam entry point checks both

@@ -617,8 +617,8 @@ def swiglu_backward_mx_checkpoint(checkpoint: MXTensor, dh: torch.Tensor, rowwis
     return dc, h
 
 
-def moe_few_tokens_workspace_bytes(tokens: int, experts: int, topk: int, F: int) -> int:
-    return int(_lib.load().moe_mx_few_tokens_workspace_bytes(int(tokens), int(experts), int(topk), int(F)))
+def moe_few_tokens_workspace_bytes(tokens: int, experts: int, topk: int, D: int, F: int) -> int:
+    return int(_lib.load().moe_mx_few_tokens_workspace_bytes(int(tokens), int(experts), int(topk), int(D), int(F)))
 
 
 def moe_mx_few_tokens(x_q: torch.Tensor, x_s: torch.Tensor, logits: torch.Tensor, topk: int, w_up_q: torch.Tensor,
@@ -645,7 +645,7 @@ def moe_mx_few_tokens(x_q: torch.Tensor, x_s: torch.Tensor, logits: torch.Tensor
     else:
         _expect(out, (T, D), torch.bfloat16, dev, "out")
     if workspace is None:
-        workspace = torch.empty(moe_few_tokens_workspace_bytes(T, E, topk, F), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(moe_few_tokens_workspace_bytes(T, E, topk, D, F), dtype=torch.uint8, device=dev)
     st = _lib.load().moe_mx_few_tokens(_at(x_q), _at(x_s), _at(logits), T, E, topk, 1 if normalize else 0,
                                        _at(w_up_q), _at(w_up_s), _at(w_down_q), _at(w_down_s), D, F, _at(out),
                                        _at(workspace), workspace.numel(), _here(dev))

@@ -56,7 +56,7 @@ SIGNATURES = {
     "swiglu_mx_quantize_checkpoint": (_I, [_P, _I64, _I64, _P, _P, _P, _P, _I, _P]),
     "swiglu_backward_mx_checkpoint": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _P]),
     "moe_mx_few_tokens": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
-    "moe_mx_few_tokens_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64]),
+    "moe_mx_few_tokens_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "grouped_wgrad_mx": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
 }
 

@@ -515,11 +515,11 @@ mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_
                                                         h_q_col, h_s_col, (int)rule, stream));
 }
 
-size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t F) {
+size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t D, int64_t F) {
     if (tokens < 0 || tokens > mxq::kMoeFewTokens || experts < 1 || experts > mxq::kMoeFewExperts || topk < 1 ||
-        topk > experts || topk > mxq::kMoeFewTopk || F < 0)
+        topk > experts || topk > mxq::kMoeFewTopk || D < 0 || F < 0 || D > (1 << 20) || F > (1 << 20))
         return 0;
-    return mxq::moe_few_workspace(tokens, experts, topk, F);
+    return mxq::moe_few_workspace(tokens, experts, topk, D, F);
 }
 
 mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float* logits, int64_t tokens,
@@ -536,7 +536,7 @@ mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float
     if (!al16(x_q) || !al16(x_s) || !al16(logits) || !al16(w_up_q) || !al16(w_up_s) || !al16(w_down_q) ||
         !al16(w_down_s) || !al16(y_bf16))
         return MXQ_ERR_ALIGN;
-    if (!workspace || workspace_bytes < mxq::moe_few_workspace(tokens, experts, topk, F)) return MXQ_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < mxq::moe_few_workspace(tokens, experts, topk, D, F)) return MXQ_ERR_WORKSPACE;
     if (!al16(workspace)) return MXQ_ERR_ALIGN;
     return hip_status(mxq::launch_moe_few(x_q, x_s, logits, w_up_q, w_up_s, w_down_q, w_down_s, tokens, experts, topk,
                                           D, F, normalize ? 1 : 0, y_bf16, workspace, stream));

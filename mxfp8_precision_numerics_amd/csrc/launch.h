@@ -97,7 +97,7 @@ hipError_t launch_swiglu_bwd_checkpoint(const uint8_t* ck_q, const uint8_t* ck_s
 
 // Routed experts of a few tokens (moe_few.hip).
 constexpr int64_t kMoeFewTokens = 64, kMoeFewExperts = 1024, kMoeFewTopk = 32;
-size_t moe_few_workspace(int64_t T, int64_t E, int64_t k, int64_t F);
+size_t moe_few_workspace(int64_t T, int64_t E, int64_t k, int64_t D, int64_t F);
 hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* logits, const uint8_t* up_q,
                           const uint8_t* up_s, const uint8_t* down_q, const uint8_t* down_s, int64_t T, int64_t E,
                           int64_t k, int64_t D, int64_t F, int normalize, uint16_t* y, void* workspace,

@@ -66,11 +66,11 @@ def test_swiglu_checkpoint_validation():
 def test_moe_few_tokens_validation():
     lib = _lib.load()
     f, size = lib.moe_mx_few_tokens, lib.moe_mx_few_tokens_workspace_bytes
-    ws = size(4, 64, 8, 128)
+    ws = size(4, 64, 8, 256, 128)
     assert ws > 4 * 8 * 128
-    for bad in ((65, 64, 8, 128), (-1, 64, 8, 128), (4, 0, 1, 128), (4, 1025, 8, 128), (4, 64, 0, 128), (4, 4, 5, 128),
-                (4, 64, 33, 128)):
-        assert size(*bad) == 0
+    for bad in ((65, 64, 8), (-1, 64, 8), (4, 0, 1), (4, 1025, 8), (4, 64, 0), (4, 4, 5), (4, 64, 33)):
+        assert size(*bad, 256, 128) == 0
+    assert size(4, 64, 8, -1, 128) == 0 and size(4, 64, 8, 256, 1 << 21) == 0
 
     def call(x=P, l=P, T=4, E=64, k=8, u=P, d=P, D=256, F=128, y=P, w=P, n=ws):
         return f(x, P, l, T, E, k, 1, u, P, d, P, D, F, y, w, n, None)

@@ -199,7 +199,7 @@ def test_graph_and_side_stream():
     T, E, k, D, F = 4, 64, 8, 256, 128
     say("few-token experts, graph")
     x, up, down, logits = _operands(T, E, D, F, 7)
-    ws = torch.empty(mxq.moe_few_tokens_workspace_bytes(T, E, k, F), dtype=torch.uint8, device=DEV)
+    ws = torch.empty(mxq.moe_few_tokens_workspace_bytes(T, E, k, D, F), dtype=torch.uint8, device=DEV)
     out = torch.empty((T, D), dtype=torch.bfloat16, device=DEV)
     mxq.moe_mx_few_tokens(*x, logits, k, *up, *down, out=out, workspace=ws)
     torch.cuda.synchronize()
