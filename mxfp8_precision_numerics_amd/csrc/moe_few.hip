@@ -424,64 +424,77 @@ __global__ __launch_bounds__(MF_DOWN_THREADS, 4) void moe_down_kernel(MoeArgs a)
 }
 
 // ---------------------------------------------------------------------------------------- many slots
-// With many slots a wave streams 64 weight rows over the whole contraction for 16 tokens of the slot, 128 values (8 KiB)
-// at a time, the next 8 KiB being on their way while it converts and multiplies; wave w of a workgroup has the slot's
-// tokens 16 w .. + 15 and leaves when there are none. (In the split form a workgroup's 128 KiB are in flight at once, but
+// With many slots a wave streams 64 weight rows over the whole contraction for 16 NT tokens of the slot, 128 values (8 KiB)
+// at a time, the next 8 KiB being on their way while it converts and multiplies. A workgroup is one wave, blockIdx.z its
+// share of the slot's tokens; those with none come last in launch order and leave at once. NT = 2, at two waves a SIMD
+// instead of three, where a slot may have more than 16 tokens, so that its weights are still read once. (In the split form a workgroup's 128 KiB are in flight at once, but
 // only two workgroups fit on a CU, and their ranking, joining and SwiGLU leave the memory idle: 85 us against 45 us for a
 // plain read of the same weights. Streaming without the second buffer, ranking, token loads, conversions and matrix
 // instructions added up to 79 us; 32 rows a wave read each token twice as often, 10 us of it.)
-constexpr int MF_STREAM_THREADS = 256;
+constexpr int MF_STREAM_THREADS = 64;
 
 // The scale bytes of a wave's 64 rows and 16 tokens wait in LDS, 2048 values' worth at a time: a load touches 16 rows
 // whatever its width, so fetching them with each 128 values made half as many requests again as the weights do.
 constexpr int MF_SPAN = 2048, MF_SCALE_WORDS = MF_SPAN / 128 + 1;            // a row's words, padded against bank conflicts
 
+template <int NT>
 struct StreamBuf {
-    uint4 v[2][4], x[2];
+    uint4 v[2][4], x[2][NT];
 };
 
+template <int NT>
 struct StreamRows {
     const uint8_t *wq[4], *ws[4];   // lane l's rows 16 i + (l % 16): codes, scales
-    const uint8_t *tq, *ts;         // lane l's token; past the slot's tokens, its first (the results are not used)
+    const uint8_t *tq[NT], *ts[NT]; // lane l's tokens; past the slot's tokens, its first (the results are not used)
     uint32_t K;
+    bool second;                    // there is a second tile of tokens
 };
 
-// The scale bytes of values k0 .. k0 + 2047 into the wave's LDS rows: 64 weight rows, then 16 tokens.
-__device__ __forceinline__ void stream_scales(const StreamRows& p, uint32_t k0, uint32_t (*lds)[MF_SCALE_WORDS]) {
+// The scale bytes of values k0 .. k0 + 2047 into the wave's LDS rows: 64 weight rows, then the tokens.
+template <int NT>
+__device__ __forceinline__ void stream_scales(const StreamRows<NT>& p, uint32_t k0, uint32_t (*lds)[MF_SCALE_WORDS]) {
     const int r = threadIdx.x & 15, g = (threadIdx.x & 63) >> 4;
     const uint32_t first = k0 / 32 + 16 * g, bytes = p.K / 32;               // this lane's 16 of the row's bytes
     if (p.K % 512 == 0) {
-        uint4 v[5];
+        uint4 v[4 + NT];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            const uint8_t* q = i < 4 ? p.ws[i] : p.ts;
+        for (int i = 0; i < 4 + NT; ++i) {
+            const uint8_t* q = i < 4 ? p.ws[i] : p.ts[i - 4];
             v[i] = make_uint4(0u, 0u, 0u, 0u);
             if (first < bytes) v[i] = *reinterpret_cast<const uint4*>(q + first);
         }
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < 4 + NT; ++i) {
             uint32_t* d = &lds[16 * i + r][4 * g];
             d[0] = v[i].x; d[1] = v[i].y; d[2] = v[i].z; d[3] = v[i].w;
         }
         return;
     }
+    // rows that do not start on 16 bytes: byte by byte, 16 in flight, repeating the row's last where it has ended
 #pragma unroll
-    for (int i = 0; i < 5; ++i) {
-        const uint8_t* q = i < 4 ? p.ws[i] : p.ts;
-        uint8_t* d = reinterpret_cast<uint8_t*>(&lds[16 * i + r][4 * g]);
-        for (int c = 0; c < 16; ++c) d[c] = first + c < bytes ? q[first + c] : (uint8_t)0;
+    for (int i = 0; i < 4 + NT; ++i) {
+        const uint8_t* q = i < 4 ? p.ws[i] : p.ts[i - 4];
+        uint32_t x[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) x[c] = q[min(first + c, bytes - 1)];
+        uint32_t* d = &lds[16 * i + r][4 * g];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) d[c] = x[4 * c] | x[4 * c + 1] << 8 | x[4 * c + 2] << 16 | x[4 * c + 3] << 24;
     }
 }
 
 // 128 values from k0. WIDE: K % 128 == 0, so every piece is whole; otherwise K % 32 == 0 and 16 bytes are whole.
-template <bool WIDE>
-__device__ __forceinline__ void stream_load(StreamBuf& b, const StreamRows& p, uint32_t k0) {
+template <bool WIDE, int NT>
+__device__ __forceinline__ void stream_load(StreamBuf<NT>& b, const StreamRows<NT>& p, uint32_t k0) {
     const uint32_t k = k0 + 16 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const bool in = WIDE || k + 64 * c < p.K;
-        b.x[c] = make_uint4(0u, 0u, 0u, 0u);
-        if (in) b.x[c] = *reinterpret_cast<const uint4*>(p.tq + k + 64 * c);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            b.x[c][t] = make_uint4(0u, 0u, 0u, 0u);
+            if (in) b.x[c][t] = *reinterpret_cast<const uint4*>(p.tq[t] + k + 64 * c);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             b.v[c][i] = make_uint4(0u, 0u, 0u, 0u);
@@ -490,35 +503,52 @@ __device__ __forceinline__ void stream_load(StreamBuf& b, const StreamRows& p, u
     }
 }
 
-__device__ __forceinline__ void stream_multiply(const StreamBuf& b, const uint32_t (*lds)[MF_SCALE_WORDS], uint32_t word,
-                                                v4f (&acc)[4]) {
+template <int NT>
+__device__ __forceinline__ void stream_multiply(const StreamBuf<NT>& b, bool second, const uint32_t (*lds)[MF_SCALE_WORDS],
+                                                uint32_t word, v4f (&acc)[NT][4]) {
     const int r = threadIdx.x & 15, sh = 8 * ((threadIdx.x & 63) >> 5);      // lane group g: byte g / 2 of a 64-value piece
-    const uint32_t xs = lds[64 + r][word];
-    uint32_t vs[4];
+    uint32_t vs[4], xs[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) xs[t] = lds[64 + 16 * t + r][word];
 #pragma unroll
     for (int i = 0; i < 4; ++i) vs[i] = lds[16 * i + r][word];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        const float xf = scale_operand((xs >> (16 * c + sh)) & 255u);
-        const bf16x8 x0 = codes_bf16(b.x[c].x, b.x[c].y, xf), x1 = codes_bf16(b.x[c].z, b.x[c].w, xf);
+        bf16x8 x0[NT], x1[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float f = scale_operand((xs[t] >> (16 * c + sh)) & 255u);
+            x0[t] = codes_bf16(b.x[c][t].x, b.x[c][t].y, f);
+            x1[t] = codes_bf16(b.x[c][t].z, b.x[c][t].w, f);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float f = scale_operand((vs[i] >> (16 * c + sh)) & 255u);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(b.v[c][i].x, b.v[c][i].y, f), x0, acc[i], 0, 0, 0);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(codes_bf16(b.v[c][i].z, b.v[c][i].w, f), x1, acc[i], 0, 0, 0);
+            const bf16x8 w0 = codes_bf16(b.v[c][i].x, b.v[c][i].y, f), w1 = codes_bf16(b.v[c][i].z, b.v[c][i].w, f);
+            acc[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x0[0], acc[0][i], 0, 0, 0);
+            acc[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x1[0], acc[0][i], 0, 0, 0);
+            if constexpr (NT == 2) {
+                if (second) {
+                    acc[1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x0[1], acc[1][i], 0, 0, 0);
+                    acc[1][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x1[1], acc[1][i], 0, 0, 0);
+                }
+            }
         }
     }
 }
 
-// acc[i] = rows 16 i + (l % 16) times the wave's tokens over K values. The wave begins `turn` steps into the contraction
+// acc[t][i] = rows 16 i + (l % 16) times the wave's tokens over K values. The wave begins `turn` steps into the contraction
 // and wraps: thousands of waves that all begin at their rows' first bytes, 2 KiB apart, would ask the same few memory
 // channels at a time.
-template <bool WIDE>
-__device__ __forceinline__ void stream_rows(const StreamRows& p, uint32_t turn, uint32_t (*lds)[MF_SCALE_WORDS], v4f (&acc)[4]) {
-    StreamBuf a, b;
+template <bool WIDE, int NT>
+__device__ __forceinline__ void stream_rows(const StreamRows<NT>& p, uint32_t turn, uint32_t (*lds)[MF_SCALE_WORDS],
+                                            v4f (&acc)[NT][4]) {
+    StreamBuf<NT> a, b;
     const uint32_t K = p.K;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = v4f{0, 0, 0, 0};
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[t][i] = v4f{0, 0, 0, 0};
     for (uint32_t base = 0; base < K; base += MF_SPAN) {
         const uint32_t steps = (min(K - base, (uint32_t)MF_SPAN) + 127) / 128;
         uint32_t at = turn % steps;
@@ -530,31 +560,30 @@ __device__ __forceinline__ void stream_rows(const StreamRows& p, uint32_t turn, 
         for (; left > 2; left -= 2) {
             const uint32_t at1 = next(at), at2 = next(at1);
             stream_load<WIDE>(b, p, base + 128 * at1);
-            stream_multiply(a, lds, at, acc);
+            stream_multiply(a, p.second, lds, at, acc);
             stream_load<WIDE>(a, p, base + 128 * at2);
-            stream_multiply(b, lds, at1, acc);
+            stream_multiply(b, p.second, lds, at1, acc);
             at = at2;
         }
         if (left == 2) {
             stream_load<WIDE>(b, p, base + 128 * next(at));
-            stream_multiply(a, lds, at, acc);
-            stream_multiply(b, lds, next(at), acc);
+            stream_multiply(a, p.second, lds, at, acc);
+            stream_multiply(b, p.second, lds, next(at), acc);
         } else {
-            stream_multiply(a, lds, at, acc);
+            stream_multiply(a, p.second, lds, at, acc);
         }
     }
 }
 
-// Up/gate and SwiGLU. Workgroup (f0, slot): 32 gate and the same 32 up rows, so h and its 32-value blocks form in a wave's
-// registers. Ranking: lane t counts how many of token t's logits precede expert e's, each wave over its share of them.
-template <int NQ, bool WIDE>
-__global__ __launch_bounds__(MF_STREAM_THREADS, 3) void moe_up_slots_kernel(MoeArgs a) {
-    __shared__ int cnt[4][MF_TOK], bad[4][MF_TOK], list[MF_TOK];
-    extern __shared__ __attribute__((aligned(16))) uint32_t scales[][80][MF_SCALE_WORDS];      // one per wave
-    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int waves = blockDim.x >> 6;
-    const int slot = blockIdx.y;
-    const bool lead = blockIdx.x == 0;
+// Up/gate and SwiGLU. Workgroup (f0, slot, tokens): 32 gate and the same 32 up rows, so h and its 32-value blocks form in
+// the wave's registers. Ranking: lane t counts how many of token t's logits precede expert e's.
+template <int NQ, bool WIDE, int NT>
+__global__ __launch_bounds__(MF_STREAM_THREADS, NT == 1 ? 3 : 2) void moe_up_slots_kernel(MoeArgs a) {
+    __shared__ int list[MF_TOK];
+    __shared__ __attribute__((aligned(16))) uint32_t scales[64 + 16 * NT][MF_SCALE_WORDS];
+    const int lane = threadIdx.x;
+    const int slot = blockIdx.y, first = 16 * NT * blockIdx.z;
+    const bool lead = blockIdx.x == 0 && blockIdx.z == 0;
     const float nan = __builtin_nanf(""), inf = __builtin_inff();
     int e = slot, t0 = 0, r0 = 0;
     if (a.pairs) {
@@ -564,42 +593,31 @@ __global__ __launch_bounds__(MF_STREAM_THREADS, 3) void moe_up_slots_kernel(MoeA
         const bool refused = row.refused();
         float value = 0.0f;
         e = refused ? -1 : __builtin_amdgcn_readfirstlane(row.expert_of(r0, value));
-        if (lead && tid == 0) a.sel[r0 * MF_TOK + t0] = refused ? nan : value;
+        if (lead && lane == 0) a.sel[r0 * MF_TOK + t0] = refused ? nan : value;
         if (e < 0) {
-            if (lead && tid == 0) a.slot_n[slot] = 0;
+            if (lead && lane == 0) a.slot_n[slot] = 0;
             return;
         }
     }
     float mine = 0.0f;
-    {
-        const int share = ((a.E + waves - 1) / waves + 3) / 4 * 4, j0 = w * share, j1 = min(a.E, j0 + share);
-        int n = 0, b = 0;
-        auto count = [&](float v, int j) {
-            n += (v > mine || (v == mine && j < e)) ? 1 : 0;
-            b |= !(v < inf) ? 1 : 0;
-        };
-        if (lane < a.T) {
-            const float* row = a.logits + lane * a.E;
-            mine = row[e];
-            if (a.E % 4 == 0) {                                              // the rows start on 16 bytes
-#pragma unroll 8
-                for (int j = j0; j < j1; j += 4) {
-                    const float4 v = *reinterpret_cast<const float4*>(row + j);
-                    count(v.x, j); count(v.y, j + 1); count(v.z, j + 2); count(v.w, j + 3);
-                }
-            } else {
-#pragma unroll 8
-                for (int j = j0; j < j1; ++j) count(row[j], j);
-            }
-        }
-        cnt[w][lane] = n;
-        bad[w][lane] = b;
-    }
-    __syncthreads();
     int rank = 0, worse = 0;
-    for (int q = 0; q < waves; ++q) {
-        rank += cnt[q][lane];
-        worse |= bad[q][lane];
+    auto count = [&](float v, int j) {
+        rank += (v > mine || (v == mine && j < e)) ? 1 : 0;
+        worse |= !(v < inf) ? 1 : 0;
+    };
+    if (lane < a.T) {
+        const float* row = a.logits + lane * a.E;
+        mine = row[e];
+        if (a.E % 4 == 0) {                                                  // the rows start on 16 bytes
+#pragma unroll 8
+            for (int j = 0; j < a.E; j += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(row + j);
+                count(v.x, j); count(v.y, j + 1); count(v.z, j + 2); count(v.w, j + 3);
+            }
+        } else {
+#pragma unroll 8
+            for (int j = 0; j < a.E; ++j) count(row[j], j);
+        }
     }
     const bool refused = worse != 0;
     const bool has = lane < a.T && !refused && rank < a.k && mine > -inf;
@@ -607,98 +625,115 @@ __global__ __launch_bounds__(MF_STREAM_THREADS, 3) void moe_up_slots_kernel(MoeA
     const bool dup = a.pairs && (who & ((1ull << t0) - 1)) != 0;              // an earlier token has this expert too
     const int n = dup ? 0 : __builtin_popcountll(who);
     const int at = __builtin_popcountll(who & ((1ull << lane) - 1));
-    if (w == 0) {
-        if (has) list[at] = lane | rank << 8;
-        if (lead) {
-            if (has) a.slot_tok[slot * MF_TOK + at] = (uint16_t)(lane | rank << 8);
-            if (!a.pairs && lane < a.T) {
-                if (refused && e < a.k) a.sel[e * MF_TOK + lane] = nan;
-                if (!refused && rank < a.k) a.sel[rank * MF_TOK + lane] = mine;
-            }
-            if (lane == 0) {
-                a.slot_e[slot] = e;
-                a.slot_n[slot] = n;
-            }
+    if (has) list[at] = lane | rank << 8;
+    if (lead) {
+        if (has) a.slot_tok[slot * MF_TOK + at] = (uint16_t)(lane | rank << 8);
+        if (!a.pairs && lane < a.T) {
+            if (refused && e < a.k) a.sel[e * MF_TOK + lane] = nan;
+            if (!refused && rank < a.k) a.sel[rank * MF_TOK + lane] = mine;
+        }
+        if (lane == 0) {
+            a.slot_e[slot] = e;
+            a.slot_n[slot] = n;
         }
     }
-    __syncthreads();
-    if (16 * w >= n) return;
+    if (first >= n) return;
+    __syncthreads();                                                         // one wave: orders the list's writes and reads
     const uint32_t D = a.D, F = a.F, f0 = blockIdx.x * 32;
     const int r = lane & 15, g = lane >> 4;
-    StreamRows rows;
+    StreamRows<NT> rows;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {                                            // gate rows 0-15, 16-31, up rows 0-15, 16-31
         const uint64_t row = (uint64_t)e * 2 * F + (i >> 1) * F + f0 + 16 * (i & 1) + r;
         rows.wq[i] = a.up_q + row * D;
         rows.ws[i] = a.up_s + row * (D / 32);
     }
-    const int tr = 16 * w + r < n ? list[16 * w + r] : -1;
-    const uint32_t token = (tr < 0 ? list[16 * w] : tr) & 255;
-    rows.tq = a.x_q + token * D;
-    rows.ts = a.x_s + token * (D / 32);
+    int tr[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int at = first + 16 * t + r;
+        tr[t] = at < n ? list[at] : -1;
+        const uint32_t token = (tr[t] < 0 ? list[first] : tr[t]) & 255;
+        rows.tq[t] = a.x_q + token * D;
+        rows.ts[t] = a.x_s + token * (D / 32);
+    }
     rows.K = D;
-    v4f acc[4];
-    stream_rows<WIDE>(rows, 5 * blockIdx.x + 3 * blockIdx.y, scales[w], acc);
-    float h[2][4];
-    uint32_t m = 0;
+    rows.second = first + 16 < n;
+    v4f acc[NT][4];
+    stream_rows<WIDE, NT>(rows, 5 * blockIdx.x + 3 * blockIdx.y, scales, acc);
 #pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {                                        // the products' output type is bf16
-            h[p][i] = swiglu_f32((float)(__bf16)acc[p][i], (float)(__bf16)acc[2 + p][i]);
-            m = max(m, __float_as_uint(h[p][i]) & 0x7FFFFFFFu);
-        }
-    const auto x = __builtin_amdgcn_permlane16_swap(m, m, false, false);     // a token's 32 values: 4 lanes of 8
-    m = max((uint32_t)x[0], (uint32_t)x[1]);
-    const auto y = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    m = max((uint32_t)y[0], (uint32_t)y[1]);
-    const uint32_t byte = mx_scale_byte_f32(m, RULE_RCEIL);
-    if (tr >= 0) {
-        const uint32_t pair = (tr & 255) * a.k + (tr >> 8);
-        uint8_t* q = a.h_q + ((uint64_t)pair * F + f0 + 4 * g);
+    for (int t = 0; t < NT; ++t) {
+        if (first + 16 * t >= n) break;
+        float h[2][4];
+        uint32_t m = 0;
 #pragma unroll
         for (int p = 0; p < 2; ++p)
-            *reinterpret_cast<uint32_t*>(q + 16 * p) = encode4(h[p][0], h[p][1], h[p][2], h[p][3], mx_inv_scale_f32(byte));
-        if (g == 0) a.h_s[pair * (F / 32) + blockIdx.x] = (uint8_t)byte;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {                                    // the products' output type is bf16
+                h[p][i] = swiglu_f32((float)(__bf16)acc[t][p][i], (float)(__bf16)acc[t][2 + p][i]);
+                m = max(m, __float_as_uint(h[p][i]) & 0x7FFFFFFFu);
+            }
+        const auto x = __builtin_amdgcn_permlane16_swap(m, m, false, false); // a token's 32 values: 4 lanes of 8
+        m = max((uint32_t)x[0], (uint32_t)x[1]);
+        const auto y = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+        m = max((uint32_t)y[0], (uint32_t)y[1]);
+        const uint32_t byte = mx_scale_byte_f32(m, RULE_RCEIL);
+        if (tr[t] >= 0) {
+            const uint32_t pair = (tr[t] & 255) * a.k + (tr[t] >> 8);
+            uint8_t* q = a.h_q + ((uint64_t)pair * F + f0 + 4 * g);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                *reinterpret_cast<uint32_t*>(q + 16 * p) = encode4(h[p][0], h[p][1], h[p][2], h[p][3], mx_inv_scale_f32(byte));
+            if (g == 0) a.h_s[pair * (F / 32) + blockIdx.x] = (uint8_t)byte;
+        }
     }
 }
 
 // Down. Workgroup (64 output columns, slot): a wave writes its tokens' products (fp32) to their pair's row;
 // moe_sum_kernel adds a token's rows in rank order. D % 64 == 32 leaves the last workgroup's upper 32 rows out: they read
 // row d0 and store nothing.
-template <bool WIDE>
-__global__ __launch_bounds__(MF_STREAM_THREADS, 3) void moe_down_slots_kernel(MoeArgs a) {
-    extern __shared__ __attribute__((aligned(16))) uint32_t scales[][80][MF_SCALE_WORDS];      // one per wave
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    const int slot = blockIdx.y;
+template <bool WIDE, int NT>
+__global__ __launch_bounds__(MF_STREAM_THREADS, NT == 1 ? 3 : 2) void moe_down_slots_kernel(MoeArgs a) {
+    __shared__ __attribute__((aligned(16))) uint32_t scales[64 + 16 * NT][MF_SCALE_WORDS];
+    const int lane = threadIdx.x;
+    const int slot = blockIdx.y, base = 16 * NT * blockIdx.z;
     const uint32_t D = a.D, F = a.F, d0 = blockIdx.x * 64;
     const int r = lane & 15, g = lane >> 4;
-    const int at = 16 * w + r;
-    const int tok = a.slot_tok[slot * MF_TOK + at];                          // past the slot's count: not used
+    int tok[NT];                                                             // past the slot's count: not used
+#pragma unroll
+    for (int t = 0; t < NT; ++t) tok[t] = a.slot_tok[slot * MF_TOK + min(base + 16 * t + r, MF_TOK - 1)];
     const int n = __builtin_amdgcn_readfirstlane(a.slot_n[slot]);
     const int e = a.pairs ? __builtin_amdgcn_readfirstlane(a.slot_e[slot]) : slot;
-    if (16 * w >= n) return;
-    StreamRows rows;
+    if (base >= n) return;
+    StreamRows<NT> rows;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint64_t row = (uint64_t)e * D + d0 + (d0 + 16 * i < D ? 16 * i : 0) + r;
         rows.wq[i] = a.down_q + row * F;
         rows.ws[i] = a.down_s + row * (F / 32);
     }
-    const bool in = at < n;
-    const int first = __builtin_amdgcn_readfirstlane(tok);                   // lane 0's token is there: 16 w < n
-    const int mine = in ? tok : first;
-    const uint32_t pair = (mine & 255) * a.k + (mine >> 8);
-    rows.tq = a.h_q + (uint64_t)pair * F;
-    rows.ts = a.h_s + (uint64_t)pair * (F / 32);
-    rows.K = F;
-    v4f acc[4];
-    stream_rows<WIDE>(rows, 5 * blockIdx.x + 3 * blockIdx.y, scales[w], acc);
-    if (!in) return;
-    float* o = a.o + ((uint64_t)pair * D + d0 + 4 * g);
+    const int first = __builtin_amdgcn_readfirstlane(tok[0]);                // lane 0's token is there: base < n
+    uint32_t pair[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (d0 + 16 * i < D) *reinterpret_cast<float4*>(o + 16 * i) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    for (int t = 0; t < NT; ++t) {
+        const int mine = base + 16 * t + r < n ? tok[t] : first;
+        pair[t] = (mine & 255) * a.k + (mine >> 8);
+        rows.tq[t] = a.h_q + (uint64_t)pair[t] * F;
+        rows.ts[t] = a.h_s + (uint64_t)pair[t] * (F / 32);
+    }
+    rows.K = F;
+    rows.second = base + 16 < n;
+    v4f acc[NT][4];
+    stream_rows<WIDE, NT>(rows, 5 * blockIdx.x + 3 * blockIdx.y, scales, acc);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        if (base + 16 * t + r >= n) continue;
+        float* o = a.o + ((uint64_t)pair[t] * D + d0 + 4 * g);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (d0 + 16 * i < D)
+                *reinterpret_cast<float4*>(o + 16 * i) = make_float4(acc[t][i][0], acc[t][i][1], acc[t][i][2], acc[t][i][3]);
+    }
 }
 
 // y[t] = sum over ranks of p o[t k + rank], in rank order: 4 columns a thread, 1024 columns of a token a workgroup. Every
@@ -766,9 +801,16 @@ hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* l
     a.o = reinterpret_cast<float*>(p);
     a.y = y;
     const dim3 up((unsigned)(F / 32), (unsigned)slots), down((unsigned)(D / 8));
-    const dim3 stream_threads((unsigned)(64 * ((T + 15) / 16)));             // a wave per 16 tokens a slot may have
-    const unsigned stream_lds = (unsigned)((T + 15) / 16) * 80 * MF_SCALE_WORDS * 4;
-    const dim3 down_slots((unsigned)((D + 63) / 64), (unsigned)slots), sum((unsigned)((D + 1023) / 1024), (unsigned)T);
+    const unsigned shares = T <= 16 ? 1 : (unsigned)((T + 31) / 32);         // of the tokens a slot may have
+    const dim3 up_slots(up.x, up.y, shares), down_slots((unsigned)((D + 63) / 64), (unsigned)slots, shares);
+    const dim3 sum((unsigned)((D + 1023) / 1024), (unsigned)T), one(MF_STREAM_THREADS);
+#define MXQ_MOE_SLOTS(NQ, NT)                                                                                        \
+    do {                                                                                                             \
+        if (D % 128 == 0) hipLaunchKernelGGL((moe_up_slots_kernel<NQ, true, NT>), up_slots, one, 0, stream, a);      \
+        else hipLaunchKernelGGL((moe_up_slots_kernel<NQ, false, NT>), up_slots, one, 0, stream, a);                  \
+        if (F % 128 == 0) hipLaunchKernelGGL((moe_down_slots_kernel<true, NT>), down_slots, one, 0, stream, a);      \
+        else hipLaunchKernelGGL((moe_down_slots_kernel<false, NT>), down_slots, one, 0, stream, a);                  \
+    } while (0)
 #define MXQ_MOE_FEW(NQ)                                                                                              \
     do {                                                                                                             \
         if (moe_few_split(slots)) {                                                                                  \
@@ -776,10 +818,8 @@ hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* l
             else hipLaunchKernelGGL((moe_up_kernel<NQ, false>), up, dim3(MF_UP_THREADS), 0, stream, a);              \
             hipLaunchKernelGGL(moe_down_kernel<NQ>, down, dim3(MF_DOWN_THREADS), 0, stream, a);                      \
         } else {                                                                                                     \
-            if (D % 128 == 0) hipLaunchKernelGGL((moe_up_slots_kernel<NQ, true>), up, stream_threads, stream_lds, stream, a); \
-            else hipLaunchKernelGGL((moe_up_slots_kernel<NQ, false>), up, stream_threads, stream_lds, stream, a);             \
-            if (F % 128 == 0) hipLaunchKernelGGL(moe_down_slots_kernel<true>, down_slots, stream_threads, stream_lds, stream, a); \
-            else hipLaunchKernelGGL(moe_down_slots_kernel<false>, down_slots, stream_threads, stream_lds, stream, a);         \
+            if (T <= 16) MXQ_MOE_SLOTS(NQ, 1);                                                                       \
+            else MXQ_MOE_SLOTS(NQ, 2);                                                                               \
             hipLaunchKernelGGL(moe_sum_kernel<NQ>, sum, dim3(256), 0, stream, a);                                    \
         }                                                                                                            \
     } while (0)
@@ -787,6 +827,7 @@ hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* l
     else if (E <= 256) MXQ_MOE_FEW(4);
     else MXQ_MOE_FEW(16);
 #undef MXQ_MOE_FEW
+#undef MXQ_MOE_SLOTS
     return hipGetLastError();
 }
 
