@@ -23,6 +23,16 @@ struct NormArgs {
     uint8_t *q_row, *s_row, *q_col, *s_col, *ck_q, *ck_s;
 };
 
+// gamma of chunk ch (zeros past the row).
+__device__ __forceinline__ void load_gamma(const float* gamma, uint32_t ch, uint32_t chunks, float (&g)[8]) {
+    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
+    if (ch < chunks) {
+        u = *reinterpret_cast<const float4*>(gamma + 8 * ch);
+        v = *reinterpret_cast<const float4*>(gamma + 8 * ch + 4);
+    }
+    g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w; g[4] = v.x; g[5] = v.y; g[6] = v.z; g[7] = v.w;
+}
+
 // ---------------------------------------------------------------------------------------- forward, row form
 // W waves per row, NCH chunks of 8 values per lane: chunk j of lane l of the row's waves is l + 64 W j, so a wave's
 // loads are contiguous and a 32-value block is one quad of lanes. W < 4 packs 4 / W rows into a workgroup.
@@ -94,6 +104,41 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void norm_row_kernel(NormArgs
     }
 }
 
+// A column pair of 32 rows of h (d[r], low half the first column), rstd rs[r], gammas g0 and g1 -> 32 codes and a scale
+// byte each. y is formed twice (for the block maximum, then for the codes) rather than kept in 64 registers.
+template <int RULE>
+__device__ __forceinline__ void encode_pair(const uint32_t (&d)[32], const float* rs, float g0, float g1, uint4 (&c0)[2],
+                                            uint4 (&c1)[2], uint32_t& b0, uint32_t& b1) {
+    float t0 = 0.0f, t1 = 0.0f;
+#pragma unroll
+    for (int r = 0; r < 32; r += 2) {
+        const float2 k = *reinterpret_cast<const float2*>(rs + r);
+        t0 = amax3(t0, (bf16_lo(d[r]) * k.x) * g0, (bf16_lo(d[r + 1]) * k.y) * g0);
+        t1 = amax3(t1, (bf16_hi(d[r]) * k.x) * g1, (bf16_hi(d[r + 1]) * k.y) * g1);
+    }
+    const uint32_t m0 = __float_as_uint(t0) & 0x7FFFFFFFu, m1 = __float_as_uint(t1) & 0x7FFFFFFFu;
+    b0 = mx_scale_byte_f32(m0, RULE);
+    b1 = mx_scale_byte_f32(m1, RULE);
+    const bool plain = block_is_plain<RULE>(m0) && block_is_plain<RULE>(m1);
+    const float s0 = plain ? scale_operand(b0) : mx_inv_scale_f32(b0), s1 = plain ? scale_operand(b1) : mx_inv_scale_f32(b1);
+    uint32_t o0[8], o1[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 k = *reinterpret_cast<const float4*>(rs + 4 * i);
+        const uint32_t* q = d + 4 * i;
+        const float y0 = (bf16_lo(q[0]) * k.x) * g0, y1 = (bf16_lo(q[1]) * k.y) * g0, y2 = (bf16_lo(q[2]) * k.z) * g0,
+                    y3 = (bf16_lo(q[3]) * k.w) * g0;
+        const float z0 = (bf16_hi(q[0]) * k.x) * g1, z1 = (bf16_hi(q[1]) * k.y) * g1, z2 = (bf16_hi(q[2]) * k.z) * g1,
+                    z3 = (bf16_hi(q[3]) * k.w) * g1;
+        o0[i] = plain ? encode4_plain(y0, y1, y2, y3, s0) : encode4(y0, y1, y2, y3, s0);
+        o1[i] = plain ? encode4_plain(z0, z1, z2, z3, s1) : encode4(z0, z1, z2, z3, s1);
+    }
+    c0[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    c0[1] = make_uint4(o0[4], o0[5], o0[6], o0[7]);
+    c1[0] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    c1[1] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
+}
+
 // ---------------------------------------------------------------------------------------- forward, column form
 // A 128 x 128 tile of h per 256-thread workgroup, through LDS: thread (p, b) reads the column pair 2p, 2p + 1 of rows
 // 32 b .. 32 b + 31 and forms y twice (for the block maximum, then for the codes) rather than keep 64 fp32 values.
@@ -113,7 +158,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
     for (int j = 0; j < 8; ++j) {
         const int lr = (tid >> 4) + 16 * j;
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (gc < cols && r0 + lr < rows) v = *reinterpret_cast<const uint4*>(h + (r0 + lr) * cols + gc);
+        if (gc < cols && r0 + lr < rows) v = ldnt16(h + (r0 + lr) * cols + gc);
         *reinterpret_cast<uint4*>(&lds[lr * (NT / 2) + 4 * ch]) = v;
     }
     if (tid < NT) rs[tid] = r0 + tid < rows ? rstd[r0 + tid] : 0.0f;
@@ -125,45 +170,20 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
     }
     __syncthreads();
     uint32_t d[32];
-    float t0 = 0.0f, t1 = 0.0f;
 #pragma unroll
-    for (int r = 0; r < 32; r += 2) {
-        d[r] = lds[(32 * b + r) * (NT / 2) + p];
-        d[r + 1] = lds[(32 * b + r + 1) * (NT / 2) + p];
-        const float2 k = *reinterpret_cast<const float2*>(&rs[32 * b + r]);
-        t0 = amax3(t0, (bf16_lo(d[r]) * k.x) * g0, (bf16_lo(d[r + 1]) * k.y) * g0);
-        t1 = amax3(t1, (bf16_hi(d[r]) * k.x) * g1, (bf16_hi(d[r + 1]) * k.y) * g1);
-    }
-    const uint32_t m0 = __float_as_uint(t0) & 0x7FFFFFFFu, m1 = __float_as_uint(t1) & 0x7FFFFFFFu;
-    const uint32_t b0 = mx_scale_byte_f32(m0, RULE), b1 = mx_scale_byte_f32(m1, RULE);
-    uint32_t o0[8], o1[8];
-    const bool plain = block_is_plain<RULE>(m0) && block_is_plain<RULE>(m1);
-    const float s0 = plain ? scale_operand(b0) : mx_inv_scale_f32(b0), s1 = plain ? scale_operand(b1) : mx_inv_scale_f32(b1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float4 k = *reinterpret_cast<const float4*>(&rs[32 * b + 4 * i]);
-        const uint32_t* q = d + 4 * i;
-        const float y0 = (bf16_lo(q[0]) * k.x) * g0, y1 = (bf16_lo(q[1]) * k.y) * g0, y2 = (bf16_lo(q[2]) * k.z) * g0,
-                    y3 = (bf16_lo(q[3]) * k.w) * g0;
-        const float z0 = (bf16_hi(q[0]) * k.x) * g1, z1 = (bf16_hi(q[1]) * k.y) * g1, z2 = (bf16_hi(q[2]) * k.z) * g1,
-                    z3 = (bf16_hi(q[3]) * k.w) * g1;
-        if (plain) {
-            o0[i] = encode4_plain(y0, y1, y2, y3, s0);
-            o1[i] = encode4_plain(z0, z1, z2, z3, s1);
-        } else {
-            o0[i] = encode4(y0, y1, y2, y3, s0);
-            o1[i] = encode4(z0, z1, z2, z3, s1);
-        }
-    }
+    for (int r = 0; r < 32; ++r) d[r] = lds[(32 * b + r) * (NT / 2) + p];
+    uint4 c0v[2], c1v[2];
+    uint32_t b0, b1;
+    encode_pair<RULE>(d, rs + 32 * b, g0, g1, c0v, c1v, b0, b1);
     __syncthreads();                                             // every column pair has been read
     uint8_t* ob = reinterpret_cast<uint8_t*>(lds);               // 128 x 128 codes, then 128 x 4 scale bytes
     const int ce = 2 * p, co = 2 * p + 1, sw = p & 7;            // 16-byte piece k of column c sits at k ^ (c/2 % 8)
     uint4* e = reinterpret_cast<uint4*>(ob + ce * NT);
     uint4* o = reinterpret_cast<uint4*>(ob + co * NT);
-    e[(2 * b) ^ sw] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-    e[(2 * b + 1) ^ sw] = make_uint4(o0[4], o0[5], o0[6], o0[7]);
-    o[(2 * b) ^ sw] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    o[(2 * b + 1) ^ sw] = make_uint4(o1[4], o1[5], o1[6], o1[7]);
+    e[(2 * b) ^ sw] = c0v[0];
+    e[(2 * b + 1) ^ sw] = c0v[1];
+    o[(2 * b) ^ sw] = c1v[0];
+    o[(2 * b + 1) ^ sw] = c1v[1];
     ob[NT * NT + 4 * ce + b] = (uint8_t)b0;
     ob[NT * NT + 4 * co + b] = (uint8_t)b1;
     __syncthreads();
@@ -178,6 +198,105 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
     if (tid < NT && c0 + tid < cols) {
         uint8_t* dst = s_col + (c0 + tid) * (rows / 32) + r0 / 32;
         for (int q = 0; q < 4 && r0 + 32 * q < rows; ++q) dst[q] = ob[NT * NT + 4 * tid + q];
+    }
+}
+
+// ---------------------------------------------------------------------------------------- forward, both forms
+// Up to 1024 columns, 32 rows of h take at most 64 KiB of LDS, two workgroups fit on a CU, and one workgroup reads its 32
+// rows once and writes everything: its waves take a row each in turn as norm_row_kernel does, and after one barrier each
+// thread encodes a column pair of the 32 rows. The four workgroups whose 32 codes share a 128-byte line of q_col run on
+// the same XCD (8 apart in launch order), whose L2 completes the line. 65536 x 512: 64 us against 67 in two passes,
+// 16384 x 1024: 34 against 38. With 2048 columns (128 KiB, one workgroup a CU) it was no faster (75 against 73 us).
+template <int RULE, int NCH, int THREADS>
+__global__ __launch_bounds__(THREADS) void norm_rows32_kernel(NormArgs a) {
+    constexpr int COLS = 512 * NCH, WAVES = THREADS / 64, PER = 32 / WAVES;
+    __shared__ __attribute__((aligned(16))) uint32_t lds[32 * COLS / 2];
+    __shared__ __attribute__((aligned(16))) float rs[32];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const uint32_t id = blockIdx.x;
+    const int64_t r0 = 32 * (4 * (int64_t)(8 * (id / 32) + id % 8) + (id / 8) % 4);
+    if (r0 >= a.rows) return;                                    // the grid is rounded up to whole groups of 32
+    const uint32_t cols = (uint32_t)a.cols, chunks = cols / 8;
+    uint4 h[PER][NCH], res[PER][NCH];
+#pragma unroll
+    for (int q = 0; q < PER; ++q)
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const uint32_t ch = lane + 64 * j;
+            const int64_t at = (r0 + w + WAVES * q) * cols + 8 * ch;
+            h[q][j] = res[q][j] = make_uint4(0u, 0u, 0u, 0u);
+            if (ch < chunks) {
+                h[q][j] = ldnt16(a.x + at);
+                if (a.res) res[q][j] = ldnt16(a.res + at);
+            }
+        }
+#pragma unroll
+    for (int q = 0; q < PER; ++q) {
+        const int lr = w + WAVES * q;
+        const int64_t row = r0 + lr;
+        float ss = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const uint32_t ch = lane + 64 * j;
+            float v[8];
+            unpack8(h[q][j], v);
+            if (a.res) {
+                float r[8];
+                unpack8(res[q][j], r);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = v[e] + r[e];
+                h[q][j] = pack8(v);
+                unpack8(h[q][j], v);
+                if (ch < chunks) stnt16(a.sum + row * cols + 8 * ch, h[q][j]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss += v[e] * v[e];
+            if (ch < chunks) *reinterpret_cast<uint4*>(&lds[lr * (COLS / 2) + 4 * ch]) = h[q][j];
+        }
+        const float rstd = 1.0f / __builtin_sqrtf(wave_sum(ss) / (float)cols + a.eps);
+        if (lane == 0) {
+            a.rstd[row] = rstd;
+            rs[lr] = rstd;
+        }
+#pragma unroll
+        for (int j = 0; j < NCH; ++j) {
+            const uint32_t ch = lane + 64 * j;
+            if (ch >= chunks) continue;                          // whole quads: cols is a multiple of 32
+            const int64_t at = row * cols + 8 * ch, sat = row * (cols / 32) + ch / 4;
+            uint32_t byte;
+            if (a.ck_q) {
+                stnt8(a.ck_q + at, encode_row8_bf16<RULE>(h[q][j], byte));
+                if ((ch & 3) == 0) a.ck_s[sat] = (uint8_t)byte;
+            }
+            if (a.q_row) {
+                float g[8], y[8];
+                load_gamma(a.gamma, ch, chunks, g);
+                unpack8(h[q][j], y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = (y[e] * rstd) * g[e];
+                stnt8(a.q_row + at, encode_row8<RULE>(y, byte));
+                if ((ch & 3) == 0) a.s_row[sat] = (uint8_t)byte;
+            }
+        }
+    }
+    __syncthreads();
+    for (uint32_t p = tid; p < cols / 2; p += THREADS) {
+        const float2 g = *reinterpret_cast<const float2*>(a.gamma + 2 * p);
+        uint32_t d[32];
+        uint4 c0[2], c1[2];
+        uint32_t b0, b1;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) d[r] = lds[r * (COLS / 2) + p];
+        encode_pair<RULE>(d, rs, g.x, g.y, c0, c1, b0, b1);
+        uint4* q = reinterpret_cast<uint4*>(a.q_col + 2 * (int64_t)p * a.rows + r0);
+        q[0] = c0[0];
+        q[1] = c0[1];
+        q = reinterpret_cast<uint4*>(a.q_col + (2 * (int64_t)p + 1) * a.rows + r0);
+        q[0] = c1[0];
+        q[1] = c1[1];
+        uint8_t* sc = a.s_col + 2 * (int64_t)p * (a.rows / 32) + r0 / 32;
+        sc[0] = (uint8_t)b0;
+        sc[a.rows / 32] = (uint8_t)b1;
     }
 }
 
@@ -228,15 +347,6 @@ __device__ __forceinline__ void load_row(BwdRow<NCH>& x, const BwdArgs& a, int64
             if constexpr (RES) x.dr[j] = ldnt16(d + 8 * ch);
         }
     }
-}
-
-__device__ __forceinline__ void load_gamma(const float* gamma, uint32_t ch, uint32_t chunks, float (&g)[8]) {
-    float4 u = make_float4(0.0f, 0.0f, 0.0f, 0.0f), v = u;
-    if (ch < chunks) {
-        u = *reinterpret_cast<const float4*>(gamma + 8 * ch);
-        v = *reinterpret_cast<const float4*>(gamma + 8 * ch + 4);
-    }
-    g[0] = u.x; g[1] = u.y; g[2] = u.z; g[3] = u.w; g[4] = v.x; g[5] = v.y; g[6] = v.z; g[7] = v.w;
 }
 
 template <int W, int NCH, bool RES>
@@ -366,8 +476,19 @@ static void run_row(const NormArgs& a, hipStream_t stream) {
                        dim3(W < 4 ? 256 : 64 * W), 0, stream, a);
 }
 
+template <int RULE, int NCH, int THREADS>
+static void run_rows32(const NormArgs& a, hipStream_t stream) {
+    hipLaunchKernelGGL((norm_rows32_kernel<RULE, NCH, THREADS>), dim3((unsigned)((a.rows / 32 + 31) / 32 * 32)), dim3(THREADS),
+                       0, stream, a);
+}
+
 template <int RULE>
 static void run_norm(const NormArgs& a, hipStream_t stream) {
+    if (a.q_col && a.cols <= 1024) {
+        if (a.cols <= 512) run_rows32<RULE, 1, 512>(a, stream);
+        else run_rows32<RULE, 2, 512>(a, stream);
+        return;
+    }
     if (a.cols <= 512) run_row<RULE, 1, 1>(a, stream);
     else if (a.cols <= 1024) run_row<RULE, 1, 2>(a, stream);
     else if (a.cols <= 2048) run_row<RULE, 1, 4>(a, stream);
