@@ -424,22 +424,28 @@ __global__ __launch_bounds__(MF_DOWN_THREADS, 4) void moe_down_kernel(MoeArgs a)
 }
 
 // ---------------------------------------------------------------------------------------- many slots
-// With many slots a wave streams 64 weight rows over the whole contraction for 16 NT tokens of the slot, 128 values (8 KiB)
-// at a time, the next 8 KiB being on their way while it converts and multiplies. A workgroup is one wave, blockIdx.z its
-// share of the slot's tokens; those with none come last in launch order and leave at once. NT = 2, at two waves a SIMD
-// instead of three, where a slot may have more than 16 tokens, so that its weights are still read once. (In the split form a workgroup's 128 KiB are in flight at once, but
-// only two workgroups fit on a CU, and their ranking, joining and SwiGLU leave the memory idle: 85 us against 45 us for a
-// plain read of the same weights. Streaming without the second buffer, ranking, token loads, conversions and matrix
-// instructions added up to 79 us; 32 rows a wave read each token twice as often, 10 us of it.)
+// With many slots a wave streams 64 weight rows over the whole contraction for 16 NT tokens of the slot, 256 / NT values at
+// a time, the next ones being on their way while it converts and multiplies. A workgroup is one wave, blockIdx.z its
+// share of the slot's tokens; those with none come last in launch order and leave at once. NT = 2 where a slot may have
+// more than 16 tokens, so that its weights are still read once. (In the split form a workgroup's 128 KiB are in flight at
+// once, but only two workgroups fit on a CU, and their ranking, joining and SwiGLU leave the memory idle: 85 us against
+// 45 us for a plain read of the same weights. Streaming without the second buffer, ranking, token loads, conversions and
+// matrix instructions added up to 79 us; 32 rows a wave read each token twice as often, 10 us of it.)
 constexpr int MF_STREAM_THREADS = 64;
 
 // The scale bytes of a wave's 64 rows and 16 tokens wait in LDS, 2048 values' worth at a time: a load touches 16 rows
 // whatever its width, so fetching them with each 128 values made half as many requests again as the weights do.
 constexpr int MF_SPAN = 2048, MF_SCALE_WORDS = MF_SPAN / 128 + 1;            // a row's words, padded against bank conflicts
 
+// 64-byte pieces of a step: two steps are in flight, 16 KiB of weights each for one tile of tokens, 8 KiB for two, which is
+// what the registers of two waves a SIMD hold. With one tile, three waves and 8 KiB a step: 90.6 us against 88.4 at 16
+// tokens of 64 experts, 2048 and 1024 columns, top 8, and 145 against 130 at 2080 and 992 columns.
+template <int NT>
+constexpr int MF_STEP = NT == 1 ? 4 : 2;
+
 template <int NT>
 struct StreamBuf {
-    uint4 v[2][4], x[2][NT];
+    uint4 v[MF_STEP<NT>][4], x[MF_STEP<NT>][NT];
 };
 
 template <int NT>
@@ -483,12 +489,12 @@ __device__ __forceinline__ void stream_scales(const StreamRows<NT>& p, uint32_t 
     }
 }
 
-// 128 values from k0. WIDE: K % 128 == 0, so every piece is whole; otherwise K % 32 == 0 and 16 bytes are whole.
+// One step from k0. WIDE: K is a whole number of steps; otherwise K % 32 == 0 and 16 bytes are whole.
 template <bool WIDE, int NT>
 __device__ __forceinline__ void stream_load(StreamBuf<NT>& b, const StreamRows<NT>& p, uint32_t k0) {
     const uint32_t k = k0 + 16 * ((threadIdx.x & 63) >> 4);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+    for (int c = 0; c < MF_STEP<NT>; ++c) {
         const bool in = WIDE || k + 64 * c < p.K;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
@@ -505,25 +511,26 @@ __device__ __forceinline__ void stream_load(StreamBuf<NT>& b, const StreamRows<N
 
 template <int NT>
 __device__ __forceinline__ void stream_multiply(const StreamBuf<NT>& b, bool second, const uint32_t (*lds)[MF_SCALE_WORDS],
-                                                uint32_t word, v4f (&acc)[NT][4]) {
+                                                uint32_t step, v4f (&acc)[NT][4]) {
     const int r = threadIdx.x & 15, sh = 8 * ((threadIdx.x & 63) >> 5);      // lane group g: byte g / 2 of a 64-value piece
-    uint32_t vs[4], xs[NT];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xs[t] = lds[64 + 16 * t + r][word];
+    for (int c = 0; c < MF_STEP<NT>; ++c) {
+        const uint32_t w = (MF_STEP<NT> / 2) * step + c / 2;                 // a word holds the scales of two pieces
+        uint32_t vs[4], xs[NT];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) vs[i] = lds[16 * i + r][word];
+        for (int t = 0; t < NT; ++t) xs[t] = lds[64 + 16 * t + r][w] >> (16 * (c & 1) + sh);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 4; ++i) vs[i] = lds[16 * i + r][w] >> (16 * (c & 1) + sh);
         bf16x8 x0[NT], x1[NT];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float f = scale_operand((xs[t] >> (16 * c + sh)) & 255u);
+            const float f = scale_operand(xs[t] & 255u);
             x0[t] = codes_bf16(b.x[c][t].x, b.x[c][t].y, f);
             x1[t] = codes_bf16(b.x[c][t].z, b.x[c][t].w, f);
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float f = scale_operand((vs[i] >> (16 * c + sh)) & 255u);
+            const float f = scale_operand(vs[i] & 255u);
             const bf16x8 w0 = codes_bf16(b.v[c][i].x, b.v[c][i].y, f), w1 = codes_bf16(b.v[c][i].z, b.v[c][i].w, f);
             acc[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0, x0[0], acc[0][i], 0, 0, 0);
             acc[0][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w1, x1[0], acc[0][i], 0, 0, 0);
@@ -544,29 +551,30 @@ template <bool WIDE, int NT>
 __device__ __forceinline__ void stream_rows(const StreamRows<NT>& p, uint32_t turn, uint32_t (*lds)[MF_SCALE_WORDS],
                                             v4f (&acc)[NT][4]) {
     StreamBuf<NT> a, b;
+    constexpr uint32_t LEN = 64 * MF_STEP<NT>;
     const uint32_t K = p.K;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[t][i] = v4f{0, 0, 0, 0};
     for (uint32_t base = 0; base < K; base += MF_SPAN) {
-        const uint32_t steps = (min(K - base, (uint32_t)MF_SPAN) + 127) / 128;
+        const uint32_t steps = (min(K - base, (uint32_t)MF_SPAN) + LEN - 1) / LEN;
         uint32_t at = turn % steps;
         auto next = [&](uint32_t x) { return x + 1 == steps ? 0u : x + 1; };
-        stream_load<WIDE>(a, p, base + 128 * at);
+        stream_load<WIDE>(a, p, base + LEN * at);
         stream_scales(p, base, lds);
         // No load stands behind a condition: where one may be skipped, a wait for the other buffer waits for all.
         uint32_t left = steps;
         for (; left > 2; left -= 2) {
             const uint32_t at1 = next(at), at2 = next(at1);
-            stream_load<WIDE>(b, p, base + 128 * at1);
+            stream_load<WIDE>(b, p, base + LEN * at1);
             stream_multiply(a, p.second, lds, at, acc);
-            stream_load<WIDE>(a, p, base + 128 * at2);
+            stream_load<WIDE>(a, p, base + LEN * at2);
             stream_multiply(b, p.second, lds, at1, acc);
             at = at2;
         }
         if (left == 2) {
-            stream_load<WIDE>(b, p, base + 128 * next(at));
+            stream_load<WIDE>(b, p, base + LEN * next(at));
             stream_multiply(a, p.second, lds, at, acc);
             stream_multiply(b, p.second, lds, next(at), acc);
         } else {
@@ -578,7 +586,7 @@ __device__ __forceinline__ void stream_rows(const StreamRows<NT>& p, uint32_t tu
 // Up/gate and SwiGLU. Workgroup (f0, slot, tokens): 32 gate and the same 32 up rows, so h and its 32-value blocks form in
 // the wave's registers. Ranking: lane t counts how many of token t's logits precede expert e's.
 template <int NQ, bool WIDE, int NT>
-__global__ __launch_bounds__(MF_STREAM_THREADS, NT == 1 ? 3 : 2) void moe_up_slots_kernel(MoeArgs a) {
+__global__ __launch_bounds__(MF_STREAM_THREADS, 2) void moe_up_slots_kernel(MoeArgs a) {
     __shared__ int list[MF_TOK];
     __shared__ __attribute__((aligned(16))) uint32_t scales[64 + 16 * NT][MF_SCALE_WORDS];
     const int lane = threadIdx.x;
@@ -693,7 +701,7 @@ __global__ __launch_bounds__(MF_STREAM_THREADS, NT == 1 ? 3 : 2) void moe_up_slo
 // moe_sum_kernel adds a token's rows in rank order. D % 64 == 32 leaves the last workgroup's upper 32 rows out: they read
 // row d0 and store nothing.
 template <bool WIDE, int NT>
-__global__ __launch_bounds__(MF_STREAM_THREADS, NT == 1 ? 3 : 2) void moe_down_slots_kernel(MoeArgs a) {
+__global__ __launch_bounds__(MF_STREAM_THREADS, 2) void moe_down_slots_kernel(MoeArgs a) {
     __shared__ __attribute__((aligned(16))) uint32_t scales[64 + 16 * NT][MF_SCALE_WORDS];
     const int lane = threadIdx.x;
     const int slot = blockIdx.y, base = 16 * NT * blockIdx.z;
@@ -806,9 +814,9 @@ hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* l
     const dim3 sum((unsigned)((D + 1023) / 1024), (unsigned)T), one(MF_STREAM_THREADS);
 #define MXQ_MOE_SLOTS(NQ, NT)                                                                                        \
     do {                                                                                                             \
-        if (D % 128 == 0) hipLaunchKernelGGL((moe_up_slots_kernel<NQ, true, NT>), up_slots, one, 0, stream, a);      \
+        if (D % (256 / NT) == 0) hipLaunchKernelGGL((moe_up_slots_kernel<NQ, true, NT>), up_slots, one, 0, stream, a); \
         else hipLaunchKernelGGL((moe_up_slots_kernel<NQ, false, NT>), up_slots, one, 0, stream, a);                  \
-        if (F % 128 == 0) hipLaunchKernelGGL((moe_down_slots_kernel<true, NT>), down_slots, one, 0, stream, a);      \
+        if (F % (256 / NT) == 0) hipLaunchKernelGGL((moe_down_slots_kernel<true, NT>), down_slots, one, 0, stream, a); \
         else hipLaunchKernelGGL((moe_down_slots_kernel<false, NT>), down_slots, one, 0, stream, a);                  \
     } while (0)
 #define MXQ_MOE_FEW(NQ)                                                                                              \
