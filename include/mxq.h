@@ -392,8 +392,8 @@ mxq_status swiglu_mx_quantize_checkpoint(const uint16_t* c_bf16, int64_t rows, i
  *   q_row, s_row, q_col, s_col: dc as in swiglu_backward_mx_quantize (rows of 2F; blocks of 32 rows down columns);
  *   h_q_col[F][rows], h_s_col[F][rows/32]: h = silu(g) u recomputed from the checkpoint, column orientation, so the
  *   forward need not keep the down projection's Wgrad operand.
- * Each pair may be NULL, not all three. A block whose scale byte is 0xFF reads back as NaN. Requires F % 32 == 0, and
- * rows % 32 == 0 when a column orientation is asked for.
+ * Each pair may be NULL, not all three. A block whose scale byte is 0xFF reads back as NaN. Requires F % 32 == 0,
+ * F <= 2^22, and rows % 32 == 0 when a column orientation is asked for.
  */
 mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_s, const uint16_t* dh_bf16,
                                          int64_t rows, int64_t F, uint8_t* q_row, uint8_t* s_row, uint8_t* q_col,

@@ -14,6 +14,8 @@ namespace mxq {
 
 // ---------------------------------------------------------------------------------------- forward
 // One 8-value chunk of g and of u per thread; a quad of lanes holds a 32-value block of each (F % 32 == 0).
+// 132160 x 1024: 170 us, 5.6 TB/s of 7.09 bytes a value of h; 52 vector instructions a value fill half its cycles, beside
+// five streams of memory. One chunk a thread over a full grid: nothing is carried from one chunk to the next.
 template <int RULE>
 __global__ __launch_bounds__(256) void swiglu_ck_fwd_kernel(const uint16_t* __restrict__ c, int64_t rows, int64_t F,
                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ s,
