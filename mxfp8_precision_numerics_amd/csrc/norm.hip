@@ -145,8 +145,9 @@ __device__ __forceinline__ void encode_pair(const uint32_t (&d)[32], const float
 // A 128 x 128 tile of h per 256-thread workgroup, through LDS: thread (p, b) reads the column pair 2p, 2p + 1 of rows
 // 32 b .. 32 b + 31 and forms y twice (for the block maximum, then for the codes) rather than keep 64 fp32 values.
 // The codes pass through LDS once more so that each column's 128 codes leave as 16-byte pieces of whole lines.
-// 3.03 bytes a value: 16384 x 2048 22.8 us (4.5 TB/s; part of h is still in the last-level cache), 4096 x 12288 32.0 us
-// (4.8 TB/s). The row form's pass leaves h in bf16, so this reads 2 bytes a value where keeping y would cost 4.
+// The codes, whole lines, go past the caches (through them 22.8 and 32.0 us for the two sizes here).
+// 3.03 bytes a value: 16384 x 2048 21.7 us (4.7 TB/s; part of h is still in the last-level cache), 4096 x 12288 30.5 us
+// (5.0 TB/s). The row form's pass leaves h in bf16, so this reads 2 bytes a value where keeping y would cost 4.
 constexpr int NT = 128;
 
 template <int RULE>
@@ -196,8 +197,8 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
     for (int pass = 0; pass < 4; ++pass) {
         const int c = 32 * pass + (tid >> 3);
         if (c0 + c < cols && r0 + 16 * k < rows)                 // rows % 32 == 0: a 16-row piece is whole
-            *reinterpret_cast<uint4*>(q_col + (c0 + c) * rows + r0 + 16 * k) =
-                *reinterpret_cast<const uint4*>(ob + c * NT + 16 * (k ^ ((c >> 1) & 7)));
+            stnt16(q_col + (c0 + c) * rows + r0 + 16 * k,
+                   *reinterpret_cast<const uint4*>(ob + c * NT + 16 * (k ^ ((c >> 1) & 7))));
     }
     if (tid < NT && c0 + tid < cols) {
         uint8_t* dst = s_col + (c0 + tid) * (rows / 32) + r0 / 32;
