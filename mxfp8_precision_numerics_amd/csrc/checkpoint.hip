@@ -14,8 +14,9 @@ namespace mxq {
 
 // ---------------------------------------------------------------------------------------- forward
 // One 8-value chunk of g and of u per thread; a quad of lanes holds a 32-value block of each (F % 32 == 0).
-// 132160 x 1024: 170 us, 5.6 TB/s of 7.09 bytes a value of h; 52 vector instructions a value fill half its cycles, beside
-// five streams of memory. One chunk a thread over a full grid: nothing is carried from one chunk to the next.
+// 132160 x 1024: 170 us, 5.6 TB/s of 7.09 bytes a value of h. 52 vector instructions a value at four cycles each take
+// about that time as well (the exponential is 21 of them, one rounding each), so memory and the vector units are both
+// near their limits. Stores through the caches: 182 us against 175 a call.
 template <int RULE>
 __global__ __launch_bounds__(256) void swiglu_ck_fwd_kernel(const uint16_t* __restrict__ c, int64_t rows, int64_t F,
                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ s,
@@ -52,11 +53,11 @@ __global__ __launch_bounds__(256) void swiglu_ck_fwd_kernel(const uint16_t* __re
 // 8 (tid % 16) .. + 7. The row orientation leaves from registers. d_gate, d_up and h go to three fp32 LDS tiles
 // (48 KiB), and after one barrier each of 3 x 128 threads encodes one column.
 //
-// Bound by memory, at 56% writes: 132160 x 1024 286 us, 4.4 TB/s of 9.22 bytes a value of h, 16384 x 8192 302 us.
-// Without the row outputs 60 us less, without the column codes 75 less, without the table's reads no less. The row codes
-// go through the L2, which joins them with their neighbours (non-temporal: 324 us); the column codes, whole lines, do not
-// (through it: 345 against 320). Values kept in registers, their column maxima by lane permutations and only codes
-// through LDS: half the LDS traffic, but 64-byte row pieces and room for no loads ahead: 370 us.
+// Bound by memory, at 56% writes: 132160 x 1024 320 us, 3.9 TB/s of 9.22 bytes a value of h, 16384 x 8192 314 us. Without
+// the row outputs 60 us less, without the column codes 75 less, without the table's reads no less. All codes go past the
+// caches: through the L2 the column codes cost 25 us, the row codes between -35 and +30 with where the buffers lie in
+// memory. Values kept in registers, their column maxima by lane permutations and only codes through LDS: half the LDS
+// traffic, but 64-byte row pieces and no room for loads ahead: 370 us.
 //
 // silu and its derivative by table: g^ is one of 256 codes times its block's scale, so for the CT_SCALES scales of
 // ordinary activations (blocks whose largest value lies between 0.007 and 448) a workgroup evaluates both once per code,
@@ -195,14 +196,14 @@ __global__ __launch_bounds__(CT_THREADS, 4) void swiglu_ck_bwd_kernel(CkBwdArgs 
         for (int e = 0; e < 8; ++e) x[e] = d[e] * silu[e];       // d_up
         put8(tile[1], rr, cc / 8, x);
         if (row_ok) {
-            *reinterpret_cast<uint2*>(qr + F + qo) = encode_row8<RULE>(x, byte);
+            stnt8(qr + F + qo, encode_row8<RULE>(x, byte));
             if ((tid & 3) == 0) sr[F / 32 + so] = (uint8_t)byte;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = (d[e] * v[e]) * slope[e];   // d_gate
         put8(tile[0], rr, cc / 8, x);
         if (row_ok) {
-            *reinterpret_cast<uint2*>(qr + qo) = encode_row8<RULE>(x, byte);
+            stnt8(qr + qo, encode_row8<RULE>(x, byte));
             if ((tid & 3) == 0) sr[so] = (uint8_t)byte;
         }
         if (!a.q_col && !a.h_q) continue;
