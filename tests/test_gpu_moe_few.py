@@ -224,6 +224,20 @@ def test_graph_and_side_stream():
     assert torch.equal(y.view(torch.int16), eager.view(torch.int16))
 
 
+@pytest.mark.parametrize("T,E,k,D,F", [
+    (2, 8, 2, 4128, 64), (1, 6, 3, 4096, 2112), (16, 24, 3, 4128, 64), (20, 24, 2, 64, 2208), (5, 40, 4, 2304, 2080),
+    (40, 20, 2, 4096, 96), (9, 32, 3, 6176, 4256),
+])
+def test_long_contractions(T, E, k, D, F):
+    """Contractions past the 2048 values that a workgroup or a wave has in hand at once, whole and with a rest."""
+    need_gpu()
+    say("few-token experts, long contractions", T, E, k, D, F)
+    x, up, down, logits = _operands(T, E, D, F, 11)
+    y = mxq.moe_mx_few_tokens(*x, logits, k, *up, *down)
+    torch.cuda.synchronize()
+    _near(y, _reference(x, up, down, logits, k, True), F)
+
+
 def test_weights_past_2_31_bytes():
     """Expert weights of 2.2e9 bytes: tokens sent to the last expert."""
     need_gpu()
