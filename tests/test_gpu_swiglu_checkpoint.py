@@ -84,6 +84,25 @@ def test_backward(rows, F, rule, row, col, hid):
         assert h is None
 
 
+@pytest.mark.parametrize("std,rule", [(1.5, mxq.RCEIL), (1e-4, mxq.FLOOR)])
+def test_backward_many_tiles(std, rule):
+    """Enough tiles for groups of four down a column, the last group and the last tile across being partial; with small
+    values no block's scale is in the kernel's table."""
+    need_gpu()
+    rows, F = 8224, 1056
+    say("swiglu checkpoint backward, many tiles", rows, F, std, rule)
+    ck = mxq.mx_quantize(workloads.normal_bf16((rows, 2 * F), std, 51, 8, DEV), colwise=False)
+    dh = workloads.normal_bf16((rows, F), 1e-3, 51, 9, DEV)
+    dc, h = mxq.swiglu_backward_mx_checkpoint(ck, dh, rule=rule)
+    torch.cuda.synchronize()
+    cb = oracle.bf16_from_f32(_values(ck.q_row, ck.s_row).astype(np.float32))
+    o = oracle.swiglu_bwd_mx_quantize(cb, u16(dh), rule, True, True)
+    assert all(np.array_equal(u8(got), want) for got, want in zip(dc, o[:4]))
+    _, _, hf = oracle.swiglu_mx_quantize(cb, rule, want_h=True)
+    w = oracle.mx_quantize_f32(hf, rule, False, True)
+    assert np.array_equal(u8(h.q_col), w[2]) and np.array_equal(u8(h.s_col), w[3])
+
+
 def test_backward_nan_block():
     need_gpu()
     say("swiglu checkpoint NaN block")
