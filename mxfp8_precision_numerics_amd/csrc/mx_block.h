@@ -103,6 +103,20 @@ __device__ __forceinline__ uint2 encode_row8_bf16(uint4 v, uint32_t& byte) {
     return make_uint2(lo, hi);
 }
 
+// The sum of N values, added in pairs, the pairs in pairs: each term passes log2 N roundings instead of up to N.
+template <int N>
+__device__ __forceinline__ float tree_sum(const float (&x)[N]) {
+    if constexpr (N == 1) {
+        return x[0];
+    } else {
+        float y[(N + 1) / 2];
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) y[i] = x[2 * i] + x[2 * i + 1];
+        if constexpr (N % 2 == 1) y[N / 2] = x[N - 1];
+        return tree_sum(y);
+    }
+}
+
 // Joins a value over the 64 lanes of a wave by lane permutations within 16-lane rows and swaps of rows and halves (no
 // LDS); every lane gets the same result, as each step joins the same two values on both sides.
 template <class Op>

@@ -1,0 +1,45 @@
+"""The norm's sum of squares on rows where the order of its additions shows.
+
+A square of a bf16 value is exact in fp32, so rstd's error is that of the additions and of four operations after them.
+Added in pairs, a sum of cols values passes ceil(log2 cols) roundings, each within u = 2^-24 of the partial sum, and all
+terms are positive: relative error at most ceil(log2 cols) u. The division by cols and the addition of eps add one each,
+the square root halves what came before it, and it and the reciprocal add one each:
+
+    |rstd / exact - 1| <= (ceil(log2 cols) / 2 + 3) u        (second-order terms are below 1e-3 u)
+
+The rows below hold a 1 at every eighth of their first columns and 2^-24 * 0.9 as square of every other value: added one
+after the other behind a 1, each of these is lost (0.9 u is less than half the spacing 2 u of numbers above 1), and a
+lane's 32 values lose 31 * 0.9 u of 1 + 31 * 0.9 u, half of which, 13.9 u, would show in rstd."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_precision_numerics_amd as mxq
+from gpu_util import DEV, need_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+SMALL = 243.0 / 256.0 * 2.0 ** -12                                # a bf16 value, its square 0.9010 u
+
+
+@pytest.mark.parametrize("rows,cols,ones,colwise,residual", [
+    (5, 2048, 512, False, False), (3, 8192, 2048, False, True), (2, 12288, 4096, False, False), (2, 32768, 8192, False, False),
+    (32, 1024, 512, True, False), (32, 992, 512, True, True), (32, 2048, 512, True, False), (1, 512, 512, False, False),
+])
+def test_rstd_of_rows_with_many_small_squares(rows, cols, ones, colwise, residual):
+    need_gpu()
+    say("rmsnorm sums", rows, cols, ones, colwise, residual)
+    x = torch.full((rows, cols), SMALL, dtype=torch.bfloat16)
+    x[:, :ones:8] = 1.0
+    x[rows - 1] *= 4.0                                            # the same bits one and a half decades up
+    res = torch.zeros_like(x).to(DEV) if residual else None
+    eps = 2.0 ** -40
+    out = mxq.rmsnorm_mx_quantize(x.to(DEV), torch.ones(cols, device=DEV), eps, residual=res, colwise=colwise)
+    torch.cuda.synchronize()
+    want = 1.0 / np.sqrt((x.double().numpy() ** 2).mean(1) + eps)
+    off = np.abs(out.rstd.double().cpu().numpy() / want - 1.0) / U
+    say("rstd off by", off.max(), "u")
+    assert np.all(off <= math.ceil(math.log2(cols)) / 2 + 3 + 1e-3)
