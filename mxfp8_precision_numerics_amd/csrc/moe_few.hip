@@ -410,6 +410,7 @@ __global__ __launch_bounds__(MF_DOWN_THREADS, 4) void moe_down_kernel(MoeArgs a)
                 y.x += pt * o[0]; y.y += pt * o[1]; y.z += pt * o[2]; y.w += pt * o[3];
                 *d = y;
             }
+            wave_lds_order();                                                // the next tile may hold this token in another lane
         }
     }
     __syncthreads();
@@ -562,7 +563,9 @@ __device__ __forceinline__ void stream_rows(const StreamRows<NT>& p, uint32_t tu
         uint32_t at = turn % steps;
         auto next = [&](uint32_t x) { return x + 1 == steps ? 0u : x + 1; };
         stream_load<WIDE>(a, p, base + LEN * at);
+        wave_lds_order();                                                    // the span before has been read
         stream_scales(p, base, lds);
+        wave_lds_order();                                                    // each lane reads words that others wrote
         // No load stands behind a condition: where one may be skipped, a wait for the other buffer waits for all.
         uint32_t left = steps;
         for (; left > 2; left -= 2) {

@@ -103,6 +103,15 @@ __device__ __forceinline__ uint2 encode_row8_bf16(uint4 v, uint32_t& byte) {
     return make_uint2(lo, hi);
 }
 
+// Orders what the lanes of a wave wrote to LDS before it and read after it, or the reverse. The hardware runs one wave's LDS
+// accesses in order, so this costs no instruction; it keeps the compiler from moving an access across, which it may where
+// it finds that no lane reads an address of its own.
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // The sum of N values, added in pairs, the pairs in pairs: each term passes log2 N roundings instead of up to N.
 template <int N>
 __device__ __forceinline__ float tree_sum(const float (&x)[N]) {

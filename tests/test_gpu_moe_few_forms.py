@@ -1,0 +1,57 @@
+"""The few-token experts through every form that a call can take: one and two tiles of tokens, whole and ragged steps and
+several spans of a contraction, up to 64, 256 and 1024 experts, few and many slots.
+
+Whole numbers. With operands of small whole numbers the first product is exact in any order, so its bf16 rounding and the
+MXFP8 of h are the oracle's byte for byte, and an expert's output keeps the product's bound 2^-20 sum |h w| before its
+share p of the sum, which is within 2^-21 (an exponential of a few ulp, a sum and a division). So
+    |y - sum p (h W^T)| <= 2^-7 |y| + 2^-19 sum p sum |h w|."""
+import numpy as np
+import pytest
+import torch
+
+import mxfp8_precision_numerics_amd as mxq
+import oracle
+from gpu_util import DEV, need_gpu, say
+from mxfp8_precision_numerics_amd import workloads
+from test_gpu_moe_few import _choice, _mx, _values
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("T,E,k,D,F", [
+    (16, 24, 2, 4128, 96),       # one tile of tokens, three spans with a rest
+    (13, 24, 2, 6144, 64),       # the same in whole steps, the second product a quarter of a step
+    (3, 64, 8, 4096, 2112),      # a slot per (token, rank); both products over two spans
+    (50, 24, 1, 4128, 2112),     # two tiles of tokens
+    (64, 20, 2, 2048, 2048),     # the same, one span each
+    (40, 200, 2, 2080, 96),      # more than 64 experts
+    (17, 300, 1, 96, 4160),      # more than 256
+    (2, 8, 4, 4128, 2112),       # few slots: two waves a slot in the second product
+    (3, 70, 5, 2080, 96),        # few slots, more than 64 experts, most waves with one slot
+    (12, 3, 3, 96, 160),         # few slots, a slot per expert: every wave's rows hold the same tokens
+])
+def test_whole_numbers_in_every_form(T, E, k, D, F):
+    need_gpu()
+    say("few-token experts, whole numbers", T, E, k, D, F)
+    rng = np.random.default_rng(T + D)
+    whole = lambda *s: torch.from_numpy(rng.integers(-2, 3, s).astype(np.float32)).to(torch.bfloat16).to(DEV)  # noqa: E731
+    x, up, down = _mx(whole(T, D)), _mx(whole(E, 2 * F, D)), _mx(whole(E, D, F))
+    logits = workloads.normal_f32((T, E), 1.0, 53, T, DEV)
+    y = mxq.moe_mx_few_tokens(*x, logits, k, *up, *down)
+    torch.cuda.synchronize()
+    got, xv = y.double().cpu().numpy(), _values(*x)
+    lg = logits.cpu().numpy().astype(np.float64)
+    want, room = np.zeros((T, D)), np.zeros((T, D))
+    chosen = _choice(lg, k)
+    for e in sorted({e for c in chosen for e in c}):
+        tok = [t for t in range(T) if e in chosen[t]]
+        c = oracle.bf16_from_f32((xv[tok] @ _values(up[0][e], up[1][e]).T).astype(np.float32))
+        q, s, _ = oracle.swiglu_mx_quantize(c)
+        h = oracle.fp8_value(q, oracle.E4M3) * np.repeat(np.ldexp(1.0, s.astype(np.int64) - 127), 32, axis=1)
+        w = _values(down[0][e], down[1][e])
+        for i, t in enumerate(tok):
+            l = lg[t][chosen[t]]
+            p = np.exp(lg[t][e] - l.max()) / np.exp(l - l.max()).sum()
+            want[t] += p * (w @ h[i])
+            room[t] += p * (np.abs(w) @ np.abs(h[i]))
+    assert np.all(np.abs(got - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -19 * room)
