@@ -547,7 +547,8 @@ __device__ __forceinline__ void stream_multiply(const StreamBuf<NT>& b, bool sec
 
 // acc[t][i] = rows 16 i + (l % 16) times the wave's tokens over K values. The wave begins `turn` steps into the contraction
 // and wraps: thousands of waves that all begin at their rows' first bytes, 2 KiB apart, would ask the same few memory
-// channels at a time.
+// channels at a time. The place depends on the expert and the rows alone, so a token meets the same order of sums wherever it
+// stands in the batch.
 template <bool WIDE, int NT>
 __device__ __forceinline__ void stream_rows(const StreamRows<NT>& p, uint32_t turn, uint32_t (*lds)[MF_SCALE_WORDS],
                                             v4f (&acc)[NT][4]) {
@@ -671,7 +672,7 @@ __global__ __launch_bounds__(MF_STREAM_THREADS, 2) void moe_up_slots_kernel(MoeA
     rows.K = D;
     rows.second = first + 16 < n;
     v4f acc[NT][4];
-    stream_rows<WIDE, NT>(rows, 5 * blockIdx.x + 3 * blockIdx.y, scales, acc);
+    stream_rows<WIDE, NT>(rows, 5 * blockIdx.x + 3 * e, scales, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if (first + 16 * t >= n) break;
@@ -735,7 +736,7 @@ __global__ __launch_bounds__(MF_STREAM_THREADS, 2) void moe_down_slots_kernel(Mo
     rows.K = F;
     rows.second = base + 16 < n;
     v4f acc[NT][4];
-    stream_rows<WIDE, NT>(rows, 5 * blockIdx.x + 3 * blockIdx.y, scales, acc);
+    stream_rows<WIDE, NT>(rows, 5 * blockIdx.x + 3 * e, scales, acc);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         if (base + 16 * t + r >= n) continue;

@@ -55,3 +55,20 @@ def test_whole_numbers_in_every_form(T, E, k, D, F):
             want[t] += p * (w @ h[i])
             room[t] += p * (np.abs(w) @ np.abs(h[i]))
     assert np.all(np.abs(got - want) <= 2.0 ** -7 * np.abs(want) + 2.0 ** -19 * room)
+
+
+@pytest.mark.parametrize("T,E,k,D,F", [(3, 64, 8, 2048, 1024), (6, 256, 8, 1056, 544), (16, 64, 8, 2048, 1024),
+                                       (20, 200, 6, 544, 1056), (40, 24, 3, 2048, 512)])
+def test_a_token_does_not_depend_on_its_place_in_the_batch(T, E, k, D, F):
+    """With more than 16 slots: the batch in another order gives the same rows in that order, byte for byte."""
+    need_gpu()
+    say("few-token experts, order of the batch", T, E, k, D, F)
+    x, up, down = (_mx(workloads.normal_bf16(s, v, 53, 300 + i, DEV)) for i, (s, v) in enumerate(
+        [((T, D), 1.0), ((E, 2 * F, D), 0.02), ((E, D, F), 0.02)]))
+    logits = workloads.normal_f32((T, E), 1.5, 53, 310, DEV)
+    y = mxq.moe_mx_few_tokens(*x, logits, k, *up, *down)
+    for order in (torch.arange(T).flip(0), torch.arange(T).roll(1), torch.from_numpy(np.random.default_rng(T).permutation(T))):
+        o = order.to(DEV)
+        z = mxq.moe_mx_few_tokens(x[0][o].contiguous(), x[1][o].contiguous(), logits[o].contiguous(), k, *up, *down)
+        torch.cuda.synchronize()
+        assert torch.equal(z.view(torch.int16), y[o].contiguous().view(torch.int16))
