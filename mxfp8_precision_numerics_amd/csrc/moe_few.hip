@@ -274,7 +274,9 @@ __global__ __launch_bounds__(MF_UP_THREADS, 4) void moe_up_kernel(MoeArgs a) {
 // these 8 weight rows twice, rows 8-15 with the other half of the contraction, and its 16 columns 8 tokens twice; the
 // two diagonal 8 x 8 quarters of the result add up to the product. Wave w takes the w-th, (w + 16)-th, ... slot that has
 // tokens (two waves a slot, half of the contraction each, while there are at most 8), and adds p times its product into
-// its own LDS rows; the 16 waves' rows are added in order at the end, so the result does not depend on timing.
+// its own LDS rows; the 16 waves' rows are added in order at the end, so the result does not depend on timing. Slots are
+// taken in the order of their experts, which is the same for every order of the batch's tokens (a single token's, in the
+// order of its ranks).
 constexpr int MF_PIECES = 4;                                                 // weight loads of a lane in flight
 
 // One slot's share of a wave: 8 rows of its weights (up to MF_PIECES 64-byte pieces of each half of the contraction), and
@@ -293,7 +295,7 @@ __global__ __launch_bounds__(MF_DOWN_THREADS, 4) void moe_down_kernel(MoeArgs a)
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const uint32_t D = a.D, F = a.F, d0 = blockIdx.x * 8;
     const int r = lane & 15, g = lane >> 4, r8 = r & 7;
-    if (w == MF_DOWN_WAVES - 1) {                                            // the slots that have tokens, in order
+    if (w == MF_DOWN_WAVES - 1) {                                            // the slots that have tokens
         int cnt[NQ], ex[NQ], before = 0;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
@@ -304,7 +306,13 @@ __global__ __launch_bounds__(MF_DOWN_THREADS, 4) void moe_down_kernel(MoeArgs a)
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             const uint64_t b = __ballot(cnt[q] > 0);
-            const int at = before + __builtin_popcountll(b & ((1ull << lane) - 1));
+            int at = before + __builtin_popcountll(b & ((1ull << lane) - 1));
+            if (q == 0 && a.pairs && a.T > 1) {                              // at most 16 slots: all in lanes 0 to 15
+                at = 0;
+#pragma unroll
+                for (int i = 0; i < MF_DOWN_WAVES; ++i)
+                    at += (b >> i & 1) && __builtin_amdgcn_readlane(ex[0], i) < ex[0] ? 1 : 0;
+            }
             if (cnt[q] > 0) {
                 live_slot[at] = 64 * q + lane;
                 live_e[at] = ex[q];

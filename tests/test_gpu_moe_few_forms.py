@@ -72,3 +72,21 @@ def test_a_token_does_not_depend_on_its_place_in_the_batch(T, E, k, D, F):
         z = mxq.moe_mx_few_tokens(x[0][o].contiguous(), x[1][o].contiguous(), logits[o].contiguous(), k, *up, *down)
         torch.cuda.synchronize()
         assert torch.equal(z.view(torch.int16), y[o].contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("T,E,k,D,F", [(2, 24, 8, 512, 256), (2, 17, 8, 2048, 1024), (5, 18, 3, 544, 96), (8, 20, 2, 256, 1056),
+                                       (4, 16, 4, 512, 256)])
+def test_place_in_the_batch_with_few_slots(T, E, k, D, F):
+    """The same with at most 16 slots; all tokens ask for much the same experts, in different orders."""
+    need_gpu()
+    say("few-token experts, order of the batch, few slots", T, E, k, D, F)
+    x, up, down = (_mx(workloads.normal_bf16(s, v, 53, 320 + i, DEV)) for i, (s, v) in enumerate(
+        [((T, D), 1.0), ((E, 2 * F, D), 0.02), ((E, D, F), 0.02)]))
+    for rep in range(8):
+        logits = workloads.normal_f32((T, E), 0.5, 53, 330 + rep, DEV)
+        logits[:, : k + 1] += 4.0
+        y = mxq.moe_mx_few_tokens(*x, logits, k, *up, *down)
+        for o in (torch.arange(T, device=DEV).flip(0), torch.arange(T, device=DEV).roll(1)):
+            z = mxq.moe_mx_few_tokens(x[0][o].contiguous(), x[1][o].contiguous(), logits[o].contiguous(), k, *up, *down)
+            torch.cuda.synchronize()
+            assert torch.equal(z.view(torch.int16), y[o].contiguous().view(torch.int16)), rep
