@@ -484,6 +484,14 @@ def _expect(t: Optional[torch.Tensor], shape, dtype, dev, name: str):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {dev}")
 
 
+def _scratch(t: torch.Tensor, dev) -> int:
+    """The bytes of a caller's workspace, which lies on the inputs' device and may be of any type. (Its length is the
+    library's to check.)"""
+    if t.device != dev or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return t.numel() * t.element_size()
+
+
 def _mx_rows(rows: int, cols: int, dev) -> MXTensor:
     """A new MXFP8 tensor in the row orientation."""
     return MXTensor(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
@@ -566,7 +574,7 @@ def rmsnorm_backward_mx_checkpoint(dy: torch.Tensor, checkpoint: MXTensor, rstd:
     st = _lib.load().rmsnorm_backward_mx_checkpoint(
         _at(dy), _at(residual_grad), _at(checkpoint.q_row), _at(checkpoint.s_row), _at(rstd), _at(gamma), rows,
         cols, _at(out), _at(dgamma), 1 if accumulate is not None else 0, _at(workspace),
-        0 if workspace is None else workspace.numel(), _here(dev))
+        0 if workspace is None else _scratch(workspace, dev), _here(dev))
     _lib.check("rmsnorm_backward_mx_checkpoint", st)
     return out, dgamma
 
@@ -648,6 +656,6 @@ def moe_mx_few_tokens(x_q: torch.Tensor, x_s: torch.Tensor, logits: torch.Tensor
         workspace = torch.empty(moe_few_tokens_workspace_bytes(T, E, topk, D, F), dtype=torch.uint8, device=dev)
     st = _lib.load().moe_mx_few_tokens(_at(x_q), _at(x_s), _at(logits), T, E, topk, 1 if normalize else 0,
                                        _at(w_up_q), _at(w_up_s), _at(w_down_q), _at(w_down_s), D, F, _at(out),
-                                       _at(workspace), workspace.numel(), _here(dev))
+                                       _at(workspace), _scratch(workspace, dev), _here(dev))
     _lib.check("moe_mx_few_tokens", st)
     return out
