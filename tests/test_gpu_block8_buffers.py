@@ -40,3 +40,17 @@ def test_workspaces(call, size):
         call(torch.empty(n - 4, dtype=torch.uint8, device=DEV))
     for good in (torch.empty(n, dtype=torch.uint8, device=DEV), torch.empty((n + 3) // 4, device=DEV)):
         assert torch.equal(call(good), want)
+
+
+def test_no_sum_without_a_residual():
+    """Buffers reused from a call with a residual: without one the result names no sum (x itself is the norm's input)."""
+    need_gpu()
+    say("norm buffers reused without a residual")
+    x, r = workloads.normal_bf16((32, 64), 1.0, 54, 3, DEV), workloads.normal_bf16((32, 64), 1.0, 54, 4, DEV)
+    gamma = torch.ones(64, device=DEV)
+    first = mxq.rmsnorm_mx_quantize(x, gamma, 1e-6, residual=r)
+    old = first.sum.clone()
+    again = mxq.rmsnorm_mx_quantize(x, gamma, 1e-6, out=first)
+    want = mxq.rmsnorm_mx_quantize(x, gamma, 1e-6)
+    assert again.sum is None and torch.equal(first.sum, old)
+    assert again.mx.q_row is first.mx.q_row and all(torch.equal(a, b) for a, b in zip(again.mx, want.mx))
