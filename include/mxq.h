@@ -353,8 +353,10 @@ mxq_status grouped_wgrad_mx(const uint8_t* a_q, const uint8_t* a_s, const uint8_
  *   checkpoint: ck_q[rows][cols], ck_s[rows][cols/32]: mxq_quantize's row orientation of h.
  * Either orientation may be NULL, not both; the checkpoint may be NULL; rstd[rows] is required. sum_bf16 may be x_bf16
  * or residual_bf16 itself (in place). gamma[cols] is fp32 (the master weight). 0 < eps < 3e38
- * (MXQ_ERR_UNSUPPORTED otherwise). Requires cols % 32 == 0 and cols <= 32768. A NaN or infinity in a row makes the
- * row's y NaN where the formula does; its blocks then carry NaN codes and the scale byte 0xFF.
+ * (MXQ_ERR_UNSUPPORTED otherwise). Requires cols % 32 == 0 and cols <= 32768, and rows * t <= 2^32 - 1024 with t = 64 up to
+ * 2048 columns, 256 up to 8192, 512 up to 12288 and 1024 beyond; with the column orientation also rows <= 128 * 65535. A
+ * NaN or infinity in a row makes the row's y NaN where the formula does; its blocks then carry NaN codes and the scale
+ * byte 0xFF.
  */
 mxq_status rmsnorm_mx_quantize(const uint16_t* x_bf16, const uint16_t* residual_bf16, const float* gamma,
                                int64_t rows, int64_t cols, float eps, uint16_t* sum_bf16, float* rstd, uint8_t* q_row,

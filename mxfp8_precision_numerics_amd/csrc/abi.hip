@@ -447,13 +447,13 @@ mxq_status rmsnorm_mx_quantize(const uint16_t* x_bf16, const uint16_t* residual_
     if (rule != MXQ_SCALE_RCEIL && rule != MXQ_SCALE_FLOOR) return MXQ_ERR_UNSUPPORTED;
     if (!(eps > 0.0f && eps < 3.0e38f)) return MXQ_ERR_UNSUPPORTED;              // NaN fails too
     if (rows < 0 || cols < 0 || cols % 32 != 0 || cols > mxq::kNormMaxCols) return MXQ_ERR_SHAPE;
-    if ((rows + 127) / 128 > kMaxGridY) return MXQ_ERR_SHAPE;
+    if (rows > mxq::norm_max_rows(cols)) return MXQ_ERR_SHAPE;
     if (rows == 0 || cols == 0) return MXQ_OK;                                   // every pointer may be NULL
     if ((q_row == nullptr) != (s_row == nullptr) || (q_col == nullptr) != (s_col == nullptr) ||
         (ck_q == nullptr) != (ck_s == nullptr) || (residual_bf16 == nullptr) != (sum_bf16 == nullptr))
         return MXQ_ERR_NULL;
     if (!q_row && !q_col) return MXQ_ERR_NULL;
-    if (q_col && rows % 32 != 0) return MXQ_ERR_SHAPE;
+    if (q_col && (rows % 32 != 0 || (rows + 127) / 128 > kMaxGridY)) return MXQ_ERR_SHAPE;
     if (!x_bf16 || !gamma || !rstd) return MXQ_ERR_NULL;
     if (!al16(x_bf16) || !al16(residual_bf16) || !al16(gamma) || !al16(sum_bf16) || !al16(rstd) || !al16(q_row) ||
         !al16(s_row) || !al16(q_col) || !al16(s_col) || !al16(ck_q) || !al16(ck_s))

@@ -77,9 +77,13 @@ hipError_t launch_adam_delayed(float* master, const uint16_t* grad, uint8_t* m_q
                                uint16_t* w, int64_t n, const AdamConsts& k, float* hist, int32_t* pos, int H,
                                float* consts, uint32_t* amax_word, hipStream_t stream);
 
+// A launch holds fewer than 2^32 threads along x; whole workgroups of up to 1024 fit below this many.
+constexpr int64_t kMaxThreads = (int64_t(1) << 32) - 1024;
+
 // RMSNorm (norm.hip). sum may be x or res; the backward writes at most kNormBwdParts partial rows of dgamma.
 constexpr int64_t kNormMaxCols = 32768;
 constexpr int64_t kNormBwdParts = 512;
+int64_t norm_max_rows(int64_t cols);   // of one forward launch
 hipError_t launch_rmsnorm_mx_quantize(const uint16_t* x, const uint16_t* res, const float* gamma, int64_t rows,
                                       int64_t cols, float eps, uint16_t* sum, float* rstd, uint8_t* q_row,
                                       uint8_t* s_row, uint8_t* q_col, uint8_t* s_col, uint8_t* ck_q, uint8_t* ck_s,

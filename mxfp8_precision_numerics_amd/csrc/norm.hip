@@ -499,6 +499,11 @@ static void run_rows32(const NormArgs& a, hipStream_t stream) {
                        0, stream, a);
 }
 
+// The row form's threads a row, by run_norm's widths.
+int64_t norm_max_rows(int64_t cols) {
+    return kMaxThreads / (cols <= 2048 ? 64 : cols <= 8192 ? 256 : cols <= 12288 ? 512 : 1024);
+}
+
 template <int RULE>
 static void run_norm(const NormArgs& a, hipStream_t stream) {
     if (a.q_col && a.cols <= 1024) {

@@ -43,3 +43,22 @@ def test_rstd_of_rows_with_many_small_squares(rows, cols, ones, colwise, residua
     off = np.abs(out.rstd.double().cpu().numpy() / want - 1.0) / U
     say("rstd off by", off.max(), "u")
     assert np.all(off <= math.ceil(math.log2(cols)) / 2 + 3 + 1e-3)
+
+
+def test_more_rows_than_the_column_form_takes():
+    """8388648 rows in the row orientation (the column one ends at 8388480): every row equals its like in a short call."""
+    need_gpu()
+    rows, cols, n = 128 * 65536 + 40, 32, 65536
+    say("rmsnorm rows", rows, cols)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(5)
+    few = torch.randn((n, cols), generator=g, device=DEV).to(torch.bfloat16)
+    gamma = 1.0 + 0.1 * torch.randn(cols, generator=g, device=DEV)
+    x = few.repeat(rows // n + 1, 1)[:rows].contiguous()
+    out = mxq.rmsnorm_mx_quantize(x, gamma, 1e-6, colwise=False)
+    want = mxq.rmsnorm_mx_quantize(few, gamma, 1e-6, colwise=False)
+    torch.cuda.synchronize()
+    for a, b in ((out.rstd, want.rstd), (out.mx.q_row, want.mx.q_row), (out.mx.s_row, want.mx.s_row),
+                 (out.checkpoint.q_row, want.checkpoint.q_row), (out.checkpoint.s_row, want.checkpoint.s_row)):
+        for r in range(0, rows, n):
+            assert torch.equal(a[r:r + n], b[:min(n, rows - r)]), r
