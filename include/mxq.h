@@ -384,7 +384,7 @@ mxq_status rmsnorm_backward_mx_checkpoint(const uint16_t* dy_bf16, const uint16_
  * which swiglu_backward_mx_checkpoint computes the gradients and the down projection's Wgrad operand:
  *   q[rows][F], s[rows][F/32]: as swiglu_mx_quantize, from the bf16 c;
  *   ck_q[rows][2F], ck_s[rows][2F/32]: mxq_quantize's row orientation of c.
- * Requires F % 32 == 0.
+ * Requires F % 32 == 0 and rows * F <= 2^35 - 2^13.
  */
 mxq_status swiglu_mx_quantize_checkpoint(const uint16_t* c_bf16, int64_t rows, int64_t F, uint8_t* q, uint8_t* s,
                                          uint8_t* ck_q, uint8_t* ck_s, mxq_scale_rule rule, hipStream_t stream);

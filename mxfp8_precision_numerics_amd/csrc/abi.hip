@@ -488,7 +488,7 @@ mxq_status swiglu_mx_quantize_checkpoint(const uint16_t* c_bf16, int64_t rows, i
     if (rule != MXQ_SCALE_RCEIL && rule != MXQ_SCALE_FLOOR) return MXQ_ERR_UNSUPPORTED;
     if (rows < 0 || F < 0 || F % 32 != 0) return MXQ_ERR_SHAPE;
     if (rows == 0 || F == 0) return MXQ_OK;
-    if ((F / 8) > (int64_t(1) << 31) || rows > (int64_t(1) << 38) / (F / 8)) return MXQ_ERR_SHAPE;   // the launch grid
+    if (rows > mxq::kMaxThreads / (F / 8)) return MXQ_ERR_SHAPE;                 // 8 values a thread
     if (!c_bf16 || !q || !s || !ck_q || !ck_s) return MXQ_ERR_NULL;
     if (!al16(c_bf16) || !al16(q) || !al16(s) || !al16(ck_q) || !al16(ck_s)) return MXQ_ERR_ALIGN;
     return hip_status(mxq::launch_swiglu_checkpoint(c_bf16, rows, F, q, s, ck_q, ck_s, (int)rule, stream));
