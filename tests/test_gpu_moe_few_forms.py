@@ -13,7 +13,7 @@ import mxfp8_precision_numerics_amd as mxq
 import oracle
 from gpu_util import DEV, need_gpu, say
 from mxfp8_precision_numerics_amd import workloads
-from test_gpu_moe_few import _choice, _mx, _values
+from test_gpu_moe_few import _choice, _mx, _near, _operands, _reference, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -90,3 +90,92 @@ def test_place_in_the_batch_with_few_slots(T, E, k, D, F):
             z = mxq.moe_mx_few_tokens(x[0][o].contiguous(), x[1][o].contiguous(), logits[o].contiguous(), k, *up, *down)
             torch.cuda.synchronize()
             assert torch.equal(z.view(torch.int16), y[o].contiguous().view(torch.int16)), rep
+
+
+@pytest.mark.parametrize("T,E,k,D,F,normalize", [
+    (1, 128, 8, 2048, 1024, True), (1, 256, 8, 544, 160, False), (2, 256, 8, 512, 96, True), (16, 200, 1, 544, 256, True),
+    (16, 200, 1, 512, 96, False),                                  # up to 16 slots, 65 to 256 experts
+    (1, 520, 4, 544, 96, True), (2, 1024, 8, 96, 160, False),      # up to 16 slots, more
+    (4, 130, 8, 512, 256, True), (12, 256, 3, 544, 96, False),     # streaming, one tile, 65 to 256 experts
+    (20, 300, 4, 512, 128, True), (33, 1000, 3, 96, 96, False), (64, 260, 2, 288, 64, True),   # two tiles, more than 256
+    (6, 600, 7, 512, 64, True),
+])
+def test_many_experts(T, E, k, D, F, normalize):
+    """The tolerance of test_gpu_moe_few.py, against its plain form."""
+    need_gpu()
+    say("few-token experts, many experts", T, E, k, D, F, normalize)
+    x, up, down, logits = _operands(T, E, D, F, 30 + k)
+    y = mxq.moe_mx_few_tokens(*x, logits, k, *up, *down, normalize=normalize)
+    torch.cuda.synchronize()
+    _near(y, _reference(x, up, down, logits, k, normalize), F)
+
+
+@pytest.mark.parametrize("T,E,k", [(3, 64, 8), (20, 16, 4), (2, 100, 5), (7, 90, 6), (5, 12, 12), (2, 300, 3)])
+@pytest.mark.parametrize("normalize", [True, False])
+def test_masks_over_chosen_and_all_logits(T, E, k, normalize):
+    """Masks that leave fewer than k experts or none, the lowest finite logit, ties, a NaN and a +inf, with the weights taken
+    over the chosen logits and over all of them."""
+    need_gpu()
+    say("few-token experts, masks", T, E, k, normalize)
+    D, F = 160, 96
+    x, up, down, _ = _operands(T, E, D, F, 40)
+    inf, low = float("inf"), torch.finfo(torch.float32).min
+    logits = workloads.normal_f32((T, E), 1.5, 53, 78, DEV)
+    kinds = {"few left": lambda l: (l[0].fill_(-inf), l[0, E - 1:].fill_(0.5), l[1, : E - 2].fill_(-inf)),
+             "none left": lambda l: (l[0].fill_(-inf), l[T - 1].fill_(-inf)),
+             "nobody": lambda l: l.fill_(-inf),
+             "lowest": lambda l: (l[0].fill_(low), l[1, 1:].fill_(low)),
+             "mask and lowest": lambda l: (l[0].fill_(-inf), l[0, 3:5].fill_(low)),
+             "ties": lambda l: (l.fill_(1.0), l[1, ::2].fill_(2.0)),
+             "far apart": lambda l: (l[0].fill_(-3e38), l[0, 2:3].fill_(3e38)),
+             "nan": lambda l: l[1, E // 2:E // 2 + 1].fill_(float("nan")),
+             "inf": lambda l: (l[0, :1].fill_(inf), l[1, E - 1:].fill_(-inf))}
+    for kind, change in kinds.items():
+        l = logits.clone()
+        change(l)
+        y = mxq.moe_mx_few_tokens(*x, l, k, *up, *down, normalize=normalize)
+        torch.cuda.synchronize()
+        say(kind)
+        with np.errstate(invalid="ignore"):
+            want = _reference(x, up, down, l, k, normalize)
+        _near(y, want, F)
+        for t, c in enumerate(_choice(l.cpu().numpy(), k)):
+            assert c != [] or bool((y[t] == 0).all())
+
+
+@pytest.mark.parametrize("T,E,k", [(2, 8, 2), (12, 8, 2), (16, 24, 2), (40, 24, 3), (2, 100, 4)])
+def test_nan_and_infinite_operands_stay_where_they_are(T, E, k):
+    """A NaN or an infinity in a token's x makes that token's row NaN; a NaN in an up weight, the rows of the tokens that chose
+    its expert; one in a down weight, its column of those rows. Every other value keeps its bytes."""
+    need_gpu()
+    say("few-token experts, NaN", T, E, k)
+    D, F = 288, 96
+    x, up, down, logits = _operands(T, E, D, F, 50)
+    clean = mxq.moe_mx_few_tokens(*x, logits, k, *up, *down)
+    chosen = _choice(logits.cpu().numpy(), k)
+    e, victim = chosen[0][k - 1], T // 2
+    near_e = torch.tensor([e in c for c in chosen], device=DEV)
+
+    def planted(pair, at, value):
+        q, s = pair[0].clone(), pair[1].clone()
+        v = torch.zeros((1, 32), dtype=torch.bfloat16, device=DEV)
+        v[0, at[-1] % 32] = value
+        m = mxq.mx_quantize(v, colwise=False)
+        b = at[-1] // 32
+        q[at[:-1]][32 * b:32 * b + 32] = m.q_row[0]
+        s[at[:-1]][b] = m.s_row[0, 0]
+        return q, s
+
+    nan, rows = float("nan"), torch.arange(T, device=DEV)
+    for name, args, bad in (
+            ("x nan", (planted(x, (victim, 37), nan), up, down), (rows == victim)[:, None].expand(T, D)),
+            ("x inf", (planted(x, (victim, 280), float("inf")), up, down), (rows == victim)[:, None].expand(T, D)),
+            ("up gate nan", (x, planted(up, (e, 5, 287), nan), down), near_e[:, None].expand(T, D)),
+            ("up nan", (x, planted(up, (e, F + 70, 0), nan), down), near_e[:, None].expand(T, D)),
+            ("down nan", (x, up, planted(down, (e, 133, 95), nan)),
+             near_e[:, None] & (torch.arange(D, device=DEV) == 133)[None])):
+        say(name)
+        y = mxq.moe_mx_few_tokens(*args[0], logits, k, *args[1], *args[2])
+        torch.cuda.synchronize()
+        assert torch.equal(torch.isnan(y), bad)
+        assert torch.equal(y[~bad].view(torch.int16), clean[~bad].view(torch.int16))
