@@ -153,18 +153,7 @@ __device__ __forceinline__ float wave_max(float v) {
 // exp_fixed without its three special cases: x is first brought into [-105, 89], outside of which the fixed sequence
 // gives 0 and infinity by itself. (A NaN becomes a number here; the quotient g / (1 + e) is a NaN all the same.)
 __device__ __forceinline__ float exp_fixed_clamped(float x) {
-    x = __builtin_amdgcn_fmed3f(x, -105.0f, 89.0f);
-    const float k = __builtin_rintf(x * 1.44269504f);
-    float r = x - k * 0.693145751953125f;
-    r = r - k * 1.42860677e-06f;
-    float p = 1.0f / 720.0f;
-    p = p * r; p = p + 1.0f / 120.0f;
-    p = p * r; p = p + 1.0f / 24.0f;
-    p = p * r; p = p + 1.0f / 6.0f;
-    p = p * r; p = p + 0.5f;
-    p = p * r; p = p + 1.0f;
-    p = p * r; p = p + 1.0f;
-    return __builtin_ldexpf(p, (int)k);
+    return exp_fixed_sequence(__builtin_amdgcn_fmed3f(x, -105.0f, 89.0f));
 }
 
 // silu[e] = g / d and sig[e] = 1 / d, d = 1 + e^-g, both correctly rounded. Markstein's division: y, one Newton step

@@ -173,11 +173,8 @@ __device__ __forceinline__ uint32_t mx_sat_threshold(uint32_t byte) {
 // A fixed fp32 sequence: Cody-Waite reduction by k ln2 (k = rint(x log2 e), ln2 split into a 16-bit high part and a
 // low part), the degree-6 Taylor polynomial of e^r in Horner form, exact scaling by 2^k. Every operation is rounded
 // on its own (callers build without contraction), so any implementation following it computes the same value; its
-// error against the true exponential is a few ulp.
-__device__ __forceinline__ float exp_fixed(float x) {
-    if (x != x) return x;
-    if (x > 88.75f) return __uint_as_float(0x7F800000u);
-    if (x < -104.0f) return 0.0f;
+// error against the true exponential is a few ulp. It takes numbers in [-105, 89]; exp_fixed takes any.
+__device__ __forceinline__ float exp_fixed_sequence(float x) {
     const float t = x * 1.44269504f;
     const float k = __builtin_rintf(t);
     const float a = k * 0.693145751953125f;
@@ -192,6 +189,13 @@ __device__ __forceinline__ float exp_fixed(float x) {
     p = p * r; p = p + 1.0f;
     p = p * r; p = p + 1.0f;
     return __builtin_ldexpf(p, (int)k);
+}
+
+__device__ __forceinline__ float exp_fixed(float x) {
+    if (x != x) return x;
+    if (x > 88.75f) return __uint_as_float(0x7F800000u);
+    if (x < -104.0f) return 0.0f;
+    return exp_fixed_sequence(x);
 }
 
 // h = silu(g) u with silu(g) = g / (1 + e^-g): one rounding per operation, in this order.
