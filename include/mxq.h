@@ -346,8 +346,9 @@ mxq_status grouped_wgrad_mx(const uint8_t* a_q, const uint8_t* a_s, const uint8_
  * projection's operands ([OLMO11] Section 11.2.1, Eq. 58, and Section 11.3.2, Eq. 60: the row orientation feeds the
  * forward product, the column orientation its Wgrad), and an 8-bit checkpoint of its input for the backward.
  *   h = bf16_rne(x + residual), written to sum_bf16; h = x when residual_bf16 is NULL (sum_bf16 must then be NULL too);
- *   rstd[r] = 1 / sqrt((sum_c h^2) / cols + eps) in fp32 (the order of the sum is the kernel's; a row whose squares
- *             overflow fp32 has rstd = 0), y = (h rstd) gamma, each operation one fp32 rounding;
+ *   rstd[r] = 1 / sqrt((sum_c h^2) / cols + eps), squares and sums of eight in fp32, the rest in 64 bits, rounded once to
+ *             fp32 (within 2.6 * 2^-24 of the exact value; a row where eight squares overflow fp32 has rstd = 0),
+ *             y = (h rstd) gamma, each operation one fp32 rounding;
  *   row:        q_row[rows][cols], s_row[rows][cols/32]: y quantized from fp32 as mxq_quantize does;
  *   column:     q_col[cols][rows], s_col[cols][rows/32]: the same down columns (needs rows % 32 == 0);
  *   checkpoint: ck_q[rows][cols], ck_s[rows][cols/32]: mxq_quantize's row orientation of h.

@@ -113,12 +113,12 @@ __device__ __forceinline__ void wave_lds_order() {
 }
 
 // The sum of N values, added in pairs, the pairs in pairs: each term passes log2 N roundings instead of up to N.
-template <int N>
-__device__ __forceinline__ float tree_sum(const float (&x)[N]) {
+template <class T, int N>
+__device__ __forceinline__ T tree_sum(const T (&x)[N]) {
     if constexpr (N == 1) {
         return x[0];
     } else {
-        float y[(N + 1) / 2];
+        T y[(N + 1) / 2];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) y[i] = x[2 * i] + x[2 * i + 1];
         if constexpr (N % 2 == 1) y[N / 2] = x[N - 1];
@@ -144,6 +144,29 @@ __device__ __forceinline__ float wave_join(float v, Op op) {
 }
 __device__ __forceinline__ float wave_sum(float v) {
     return wave_join(v, [](float a, float b) { return a + b; });
+}
+// The same sum in 64 bits, the two words of a value moved alike.
+__device__ __forceinline__ double wave_sum(double v) {
+    auto join = [](uint2 a, uint2 b) {
+        return __builtin_bit_cast(double, a) + __builtin_bit_cast(double, b);
+    };
+    auto dpp = [&](double x, auto ctrl) {
+        const uint2 w = __builtin_bit_cast(uint2, x);
+        return join(w, make_uint2((uint32_t)__builtin_amdgcn_mov_dpp((int)w.x, decltype(ctrl)::value, 0xF, 0xF, false),
+                                  (uint32_t)__builtin_amdgcn_mov_dpp((int)w.y, decltype(ctrl)::value, 0xF, 0xF, false)));
+    };
+    v = dpp(v, std::integral_constant<int, 0xB1>{});
+    v = dpp(v, std::integral_constant<int, 0x4E>{});
+    v = dpp(v, std::integral_constant<int, 0x141>{});
+    v = dpp(v, std::integral_constant<int, 0x140>{});
+    uint2 w = __builtin_bit_cast(uint2, v);
+    const auto rl = __builtin_amdgcn_permlane16_swap(w.x, w.x, false, false);
+    const auto rh = __builtin_amdgcn_permlane16_swap(w.y, w.y, false, false);
+    v = join(make_uint2((uint32_t)rl[0], (uint32_t)rh[0]), make_uint2((uint32_t)rl[1], (uint32_t)rh[1]));
+    w = __builtin_bit_cast(uint2, v);
+    const auto hl = __builtin_amdgcn_permlane32_swap(w.x, w.x, false, false);
+    const auto hh = __builtin_amdgcn_permlane32_swap(w.y, w.y, false, false);
+    return join(make_uint2((uint32_t)hl[0], (uint32_t)hh[0]), make_uint2((uint32_t)hl[1], (uint32_t)hh[1]));
 }
 __device__ __forceinline__ float wave_max(float v) {
     return wave_join(v, [](float a, float b) { return __builtin_fmaxf(a, b); });

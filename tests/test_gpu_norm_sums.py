@@ -62,3 +62,28 @@ def test_more_rows_than_the_column_form_takes():
                  (out.checkpoint.q_row, want.checkpoint.q_row), (out.checkpoint.s_row, want.checkpoint.s_row)):
         for r in range(0, rows, n):
             assert torch.equal(a[r:r + n], b[:min(n, rows - r)]), r
+
+
+@pytest.mark.parametrize("rows,cols,colwise", [
+    (4096, 2048, False), (2048, 8192, False), (1024, 12288, False), (512, 16384, False), (64, 32768, True), (4096, 512, True),
+    (2048, 992, True), (2048, 96, False), (1024, 4128, True),
+])
+def test_rstd_is_the_exact_value_rounded(rows, cols, colwise):
+    """Eight squares are added in pairs in fp32 (three roundings, at most 3 u, half of which reaches rstd), everything after
+    that in 64 bits (below 1e-3 u), and rstd is rounded once: |rstd / exact - 1| <= 2.5 u + 1e-3 u."""
+    need_gpu()
+    say("rmsnorm rstd", rows, cols, colwise)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(cols)
+    x = torch.randn((rows, cols), generator=g, device=DEV) * torch.exp2(torch.arange(rows, device=DEV) % 23 - 11)[:, None]
+    x = x.to(torch.bfloat16)
+    x[:, :: cols // 4] *= 20.0
+    x[0] = SMALL
+    x[0, ::8] = 1.0
+    out = mxq.rmsnorm_mx_quantize(x, torch.ones(cols, device=DEV), 1e-6, colwise=colwise, checkpoint=False)
+    torch.cuda.synchronize()
+    eps = float(torch.tensor(1e-6, dtype=torch.float32))
+    want = 1.0 / (x.double().square().mean(1) + eps).sqrt()
+    off = (out.rstd.double() / want - 1.0).abs() / U
+    say("rstd off by", float(off.max()), "u, root mean square", float(off.square().mean().sqrt()))
+    assert float(off.max()) <= 2.5 + 1e-3
