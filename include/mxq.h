@@ -409,12 +409,15 @@ mxq_status swiglu_backward_mx_checkpoint(const uint8_t* ck_q, const uint8_t* ck_
  *   the topk largest logits (fp32[tokens][experts]) choose its experts, equal logits by the lower index; p = the softmax
  *   of the chosen logits (normalize != 0) or their share of the softmax over all logits (normalize == 0);
  *   c = bf16_rne(x W_up[e]^T), h = swiglu_mx_quantize(c) (rceil), y[t] = bf16_rne(sum_e p_e (h W_down[e]^T)),
- * the products on the values the MXFP8 operands stand for, with fp32 accumulation and bf16-exact factors: the
- * arithmetic of grouped_scaled_gemm and swiglu_mx_quantize, so decoding sees the numbers of the training forward.
+ * the products on the values the MXFP8 operands stand for, with fp32 accumulation and bf16-exact factors. That is the
+ * arithmetic of grouped_scaled_gemm and swiglu_mx_quantize, in another order of the sums, and with the experts' outputs
+ * kept in fp32 until they are added where the grouped path rounds each to bf16: a row agrees with the training forward's
+ * but for these roundings, not bit for bit.
  *   x_q[tokens][D], x_s[tokens][D/32]; w_up_q[experts][2F][D] (gate rows, then up rows), w_up_s[experts][2F][D/32];
  *   w_down_q[experts][D][F], w_down_s[experts][D][F/32]: the row-orientation weight caches; y_bf16[tokens][D].
  * A logit of -inf is never chosen (a token with fewer than topk finite logits uses those; one with none gets a row of
- * zeros); a NaN or +inf among a token's logits makes its row NaN. Results do not depend on timing.
+ * zeros); a NaN or +inf among a token's logits makes its row NaN. Results do not depend on timing, nor a
+ * token's row on its place in the batch; which and how many others are in the batch may change the order of its sums.
  * Requires experts <= 1024, 1 <= topk <= min(experts, 32), D and F positive multiples of 32 up to 2^20. workspace:
  * moe_mx_few_tokens_workspace_bytes(tokens, experts, topk, D, F) bytes, clobbered; that call returns 0 for sizes out of
  * range.

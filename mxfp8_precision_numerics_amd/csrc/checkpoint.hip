@@ -53,16 +53,18 @@ __global__ __launch_bounds__(256) void swiglu_ck_fwd_kernel(const uint16_t* __re
 // 8 (tid % 16) .. + 7. The row orientation leaves from registers. d_gate, d_up and h go to three fp32 LDS tiles
 // (48 KiB), and after one barrier each of 3 x 128 threads encodes one column.
 //
-// Bound by memory, at 56% writes: 132160 x 1024 320 us, 3.9 TB/s of 9.22 bytes a value of h, 16384 x 8192 314 us. Without
-// the row outputs 60 us less, without the column codes 75 less, without the table's reads no less. All codes go past the
-// caches: through the L2 the column codes cost 25 us, the row codes between -35 and +30 with where the buffers lie in
-// memory. Values kept in registers, their column maxima by lane permutations and only codes through LDS: half the LDS
-// traffic, but 64-byte row pieces and no room for loads ahead: 370 us.
+// 132160 x 1024: 320 us, 3.9 TB/s of 9.22 bytes a value of h, 56% of it writes; 16384 x 8192 314 us. Nothing is saturated:
+// vector issue 0.42 of the cycles, LDS a third, waves waiting 0.41 of theirs. Without the row outputs 60 us less, without the
+// column codes 75 less, both at fewer bytes a second, without the table's reads no less: two workgroups a CU (80 KiB of LDS
+// each) take turns between the phases behind their barriers. 8 bytes a lane spill. All codes go past the caches: through
+// the L2 the column codes cost 25 us, the row codes between -35 and +30 with where the buffers lie in memory. Values kept in
+// registers, their column maxima by lane permutations and only codes through LDS: half the LDS traffic, but 64-byte row
+// pieces and no room for loads ahead: 370 us.
 //
 // silu and its derivative by table: g^ is one of 256 codes times its block's scale, so for the CT_SCALES scales of
 // ordinary activations (blocks whose largest value lies between 0.007 and 448) a workgroup evaluates both once per code,
 // 4096 pairs in 32 KiB of LDS, and reads them back in place of some 40 instructions a value. A wave that meets another
-// scale evaluates its values directly; both ways give the same bits.
+// scale (a block of zeros has one) evaluates its values directly, 384 us if all do; both ways give the same bits.
 constexpr int CT_ROWS = 32, CT_COLS = 128, CT_THREADS = 512;
 constexpr int CT_SCALES = 16, CT_SCALE0 = 112;
 constexpr int64_t CT_GRID = 512;                               // two workgroups (2 x 80 KiB of LDS) per CU

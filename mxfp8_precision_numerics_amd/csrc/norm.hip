@@ -58,8 +58,8 @@ __device__ __forceinline__ float rstd_of(double ss, double inv_cols, float eps) 
 // ---------------------------------------------------------------------------------------- forward, row form
 // W waves per row, NCH chunks of 8 values per lane: chunk j of lane l of the row's waves is l + 64 W j, so a wave's
 // loads are contiguous and a 32-value block is one quad of lanes. W < 4 packs 4 / W rows into a workgroup.
-// Bound by memory: with the residual and the checkpoint 8.06 bytes a value, 16384 x 2048 in 47.7 us (5.7 TB/s), 4096 x 12288
-// in 68.6 us (5.9 TB/s).
+// Bound by memory: with the residual and the checkpoint 8.06 bytes a value, 16384 x 2048 in 48.5 us (5.6 TB/s), 4096 x 12288
+// in 67.5 us (6.0 TB/s). The widths of a variant were chosen at its upper end.
 template <int RULE, int W, int NCH>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void norm_row_kernel(NormArgs a) {
     constexpr int ROWS = W < 4 ? 4 / W : 1;              // rows per workgroup
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(256) void norm_col_kernel(const uint16_t* h, const 
 // rows once and writes everything: its waves take a row each in turn as norm_row_kernel does, and after one barrier each
 // thread encodes a column pair of the 32 rows. The four workgroups whose 32 codes share a 128-byte line of q_col run on
 // the same XCD (8 apart in launch order), whose L2 completes the line. 65536 x 512: 64 us against 67 in two passes,
-// 16384 x 1024: 34 against 38. With 2048 columns (128 KiB, one workgroup a CU) it was no faster (75 against 73 us).
+// 16384 x 1024: 35 against 38. With 2048 columns (128 KiB, one workgroup a CU) it was no faster (75 against 73 us).
 template <int RULE, int NCH, int THREADS>
 __global__ __launch_bounds__(THREADS) void norm_rows32_kernel(NormArgs a) {
     constexpr int COLS = 512 * NCH, WAVES = THREADS / 64, PER = 32 / WAVES;
@@ -332,7 +332,8 @@ __global__ __launch_bounds__(THREADS) void norm_rows32_kernel(NormArgs a) {
 // sums, then for dx) rather than kept. Each lane keeps gamma and its columns' dgamma sums in registers over all its rows;
 // the workgroup writes one partial row of dgamma at the end, and norm_dgamma_kernel adds the partial rows in a fixed
 // order, so the result does not depend on timing. Rows too wide for that in the registers of 16 waves (two chunks a lane) read
-// gamma again for each row and load nothing ahead.
+// gamma again for each row and load nothing ahead; beyond 16384 columns (four chunks) the dgamma sums and the row exceed
+// the registers all the same and 120 bytes a lane spill: 4096 x 32768 317 us (3.0 TB/s), 4096 x 16384 100 us (4.7).
 // Bound by memory: 4096 x 12288 with the residual's gradient 67.0 us (5.3 TB/s of 7.03 bytes a value); with dgamma's
 // second launch, 4.7 us, it is the two launches that a call of 333 x 1056 consists of (3.6 and 4.1 us).
 template <int NCH>
