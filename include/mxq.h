@@ -429,6 +429,90 @@ mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float
                              hipStream_t stream);
 size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_t topk, int64_t D, int64_t F);
 
+/*
+ * Quantization of each row of a bf16 matrix x[rows][cols] to 8-bit integers: a token of an activation, or an output
+ * channel of a weight W[N][K]. With amax = max_c |x[r][c]|:
+ *   scale[r] = amax / 127 (fp32 division);  q[r][c] = the whole number nearest to 127 x[r][c] / amax, ties to even, so
+ *   -127 <= q <= 127 and x ~ q scale.
+ * An all-zero row has scale 0 and zero codes; a row holding a NaN or an infinity has a NaN scale and zero codes, so that
+ * every product with it is NaN. Requires cols % 32 == 0, and rows * t <= 2^32 - 1024 with t = 64 up to 2048 columns, 256 up
+ * to 8192 and 1024 beyond. scale needs 4-byte alignment.
+ */
+mxq_status int8_quantize_tokens(const uint16_t* x_bf16, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                                hipStream_t stream);
+
+/*
+ * Product of 8-bit integer operands with a scale for each token (row of A) and each output channel (row of B):
+ *   s[m][n] = sum_k a_q[m][k] b_q[n][k], exact;  y[m][n] = (fp32(s) a_scale[m]) b_scale[n], each operation one fp32 rounding;
+ *   swiglu == 0: c_bf16[M][N] = bf16_rne(y);
+ *   swiglu != 0: N = 2F, B holds the F gate rows, then the F up rows:  c_bf16[M][F] = bf16_rne(silu(g) u) with
+ *   g = y[m][f], u = y[m][F + f] in fp32 and silu as in swiglu_mx_quantize.
+ * Both operands are K-contiguous; rows of c_bf16 have stride ldc >= its columns. Any codes (-128 too) and any M and N (N even
+ * with swiglu). Requires K % 32 == 0 and 0 < K < 131072 (every sum then fits 32 bits). c_bf16 needs 2-byte and the scales
+ * 4-byte alignment. A result does not depend on M, on the row's place, or on timing: the sum is exact. No workspace.
+ */
+mxq_status int8_scaled_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int64_t M,
+                            int64_t N, int64_t K, int swiglu, uint16_t* c_bf16, int64_t ldc, hipStream_t stream);
+
+/*
+ * int8_scaled_gemm over ragged expert groups, of any number of rows each (none, too; no padding):
+ *   group_offsets: device int64[G+1], non-decreasing, within [0, total_rows]. Rows [offsets[g], offsets[g+1]) of c_bf16 are
+ *   those rows of A times B[g]^T; rows outside every group are left as they were.
+ *   a_q[total_rows][K], a_scale[total_rows]; b_q[G][N][K], b_scale[G][N]; c_bf16[total_rows][N], or [F] with swiglu, rows of
+ *   stride ldc.
+ * Requires what int8_scaled_gemm does, and 1 <= G <= 4096. The offsets are read on the device only; offsets that break the
+ * rule are clamped, so they give wrong rows but no stray access.
+ */
+mxq_status int8_grouped_gemm(const int8_t* a_q, const float* a_scale, const int64_t* group_offsets, int64_t G,
+                             int64_t total_rows, const int8_t* b_q, const float* b_scale, int64_t N, int64_t K, int swiglu,
+                             uint16_t* c_bf16, int64_t ldc, hipStream_t stream);
+
+/*
+ * RMSNorm of every query and key head and the rotation by position, in one pass from a QKV projection's output to
+ * attention's inputs. qkv_bf16[tokens][ld]: heads_q query heads, then heads_k key heads, of head_dim values each; what follows
+ * (the values) is not read. Per token and head, in fp32 from the bf16 values to the one rounding of the result:
+ *   rstd = 1 / sqrt(sum_d x^2 / head_dim + eps), n = (x rstd) gamma, gamma[head_dim] fp32 the same for all heads of a kind;
+ *   gamma_q and gamma_k both NULL: no norm, n = x (eps is then ignored);
+ *   pair i (i < rot / 2) of a head's first `rot` values turns by position * inv_freq[i]:
+ *     interleaved == 0: values i and rot / 2 + i;  interleaved != 0: values 2i and 2i + 1;
+ *     (a, b) -> (a cos - b sin, b cos + a sin);  values past rot are n.
+ *   position = positions[pair_axis[i]][token]: positions is a device int64[axes][tokens] (time, height and width of images and
+ *   video, say), pair_axis a HOST array of rot / 2 bytes (NULL: axis 0 for all). inv_freq is a device fp32[rot / 2]. Angles are
+ *   reduced in 64 bits with the products' roundings kept: cos and sin are within 2^-23 for |position inv_freq| < 2^50.
+ * Value d of head h of token t goes to q_bf16[t q_token_stride + h q_head_stride + d], keys likewise: token-major, head-major
+ * or rows of a cache. The outputs may be the heads' own places in qkv_bf16 (in place).
+ * A NaN in a head makes the head NaN with a norm, its pair without; where squares overflow fp32, rstd is 0.
+ * Requires head_dim a multiple of 16 up to 256, rot a multiple of 16 up to head_dim (0: no rotation), 1 <= axes <= 4,
+ * pair_axis[i] < axes, 0 <= heads <= 65536, tokens <= 2^25, ld and the strides (where there is more than one token or
+ * head) multiples of 8, ld at least the heads' width, strides at least head_dim, and 0 < eps < 3e38 with a norm. positions
+ * needs 8-byte and inv_freq 4-byte alignment.
+ */
+mxq_status qk_norm_rope(const uint16_t* qkv_bf16, int64_t ld, int64_t tokens, int64_t heads_q, int64_t heads_k,
+                        int64_t head_dim, const float* gamma_q, const float* gamma_k, float eps, const int64_t* positions,
+                        int64_t axes, const float* inv_freq, int64_t rot, const uint8_t* pair_axis, int interleaved,
+                        uint16_t* q_bf16, int64_t q_token_stride, int64_t q_head_stride, uint16_t* k_bf16,
+                        int64_t k_token_stride, int64_t k_head_stride, hipStream_t stream);
+
+/*
+ * Backward of qk_norm_rope from its input: dq and dk are the gradients of its outputs (strides as there). With d the gradient
+ * turned back, xh = x rstd (recomputed) and t = d gamma:
+ *   dqkv_bf16[tokens][ld_d], the heads laid out as in qkv_bf16: bf16_rne(rstd (t - xh (sum_d t xh) / head_dim)), or bf16_rne(d)
+ *   without a norm; columns past the heads are left as they were (attention's backward writes the values' gradient there);
+ *   dgamma_q, dgamma_k (fp32[head_dim], both or neither): sum over tokens and heads of d xh; accumulate != 0 adds it. The
+ *   sums are formed in a fixed order.
+ * qkv_bf16 may be NULL without a norm (dgamma must then be NULL). dqkv_bf16 may be qkv_bf16 itself. workspace:
+ * mxq_workspace_bytes("qk_norm_backward", head_dim) bytes, clobbered (needed only for dgamma). With no tokens dgamma is zeroed
+ * (or left alone when accumulating). Requirements as for qk_norm_rope.
+ */
+mxq_status qk_norm_rope_backward(const uint16_t* dq_bf16, int64_t dq_token_stride, int64_t dq_head_stride,
+                                 const uint16_t* dk_bf16, int64_t dk_token_stride, int64_t dk_head_stride,
+                                 const uint16_t* qkv_bf16, int64_t ld, int64_t tokens, int64_t heads_q, int64_t heads_k,
+                                 int64_t head_dim, const float* gamma_q, const float* gamma_k, float eps,
+                                 const int64_t* positions, int64_t axes, const float* inv_freq, int64_t rot,
+                                 const uint8_t* pair_axis, int interleaved, uint16_t* dqkv_bf16, int64_t ld_d,
+                                 float* dgamma_q, float* dgamma_k, int accumulate, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream);
+
 /* Adam hyper-parameters, passed by HOST pointer. step is the 1-based step count t (MXQ_ERR_SHAPE if below 1);
  * beta1 and beta2 lie in [0, 1) (MXQ_ERR_UNSUPPORTED otherwise, NaN included). Every Adam entry point checks both
  * before its early return for an empty tensor, so a call with n == 0 still reports a bad setting. */
@@ -485,7 +569,7 @@ mxq_status fp8_adam_step_delayed(float* master, const uint16_t* grad_bf16, uint8
                                  size_t workspace_bytes, hipStream_t stream);
 
 /* Workspace bytes needed by op ("pertensor", "adam", "pertensor_delayed", "adam_delayed" or "autoscale") for n
- * elements, or by "rmsnorm_backward" for n columns; 0 for an unknown op. op is a host string. */
+ * elements, by "rmsnorm_backward" for n columns, or by "qk_norm_backward" for heads of n values; 0 for an unknown op. op is a host string. */
 size_t mxq_workspace_bytes(const char* op, int64_t n);
 
 #ifdef __cplusplus

@@ -17,6 +17,12 @@ outputs, and call the C ABI of libmxq.so with raw pointers. All arithmetic happe
   swiglu_mx_quantize_checkpoint, swiglu_backward_mx_checkpoint
                          SwiGLU + MX quantize with an 8-bit checkpoint of its input, and its backward from it
   moe_mx_few_tokens      the routed experts of up to 64 tokens, from router logits to the weighted sum
+  int8_quantize_tokens   8-bit integers with one scale for each row (a token, or an output channel of a weight)
+  int8_scaled_gemm, int8_grouped_gemm
+                         C = A B^T of int8 operands with a scale for each token and output channel, optionally with SwiGLU
+                         in the same pass; dense, or over ragged expert groups of any number of rows
+  qk_norm_rope, qk_norm_rope_backward
+                         RMSNorm of every query and key head with the rotation by position (on several axes) in one pass
 """
 from __future__ import annotations
 
@@ -33,6 +39,8 @@ __all__ = ["mx_quantize", "mx_quantize_ranged", "pertensor_quantize", "scaled_ge
            "grouped_scaled_gemm_strided", "grouped_wgrad_mx",
            "rmsnorm_mx_quantize", "rmsnorm_backward_mx_checkpoint", "swiglu_mx_quantize_checkpoint",
            "swiglu_backward_mx_checkpoint", "moe_mx_few_tokens", "RMSNormOut",
+           "int8_quantize_tokens", "int8_scaled_gemm", "int8_grouped_gemm", "Int8Tensor",
+           "qk_norm_rope", "qk_norm_rope_backward", "QKNormGrads",
            "workspace_bytes", "MXTensor", "AdamHParams", "MXQError", "E4M3", "E5M2", "RCEIL", "FLOOR",
            "PER_TENSOR", "MX_BLOCK32"]
 
@@ -661,3 +669,201 @@ def moe_mx_few_tokens(x_q: torch.Tensor, x_s: torch.Tensor, logits: torch.Tensor
                                        _at(workspace), _scratch(workspace, dev), _here(dev))
     _lib.check("moe_mx_few_tokens", st)
     return out
+
+
+class Int8Tensor(NamedTuple):
+    """Codes and the scale of each row (a token, or an output channel): x ~ q * scale[:, None]."""
+    q: torch.Tensor                     # int8 [rows][cols]
+    scale: torch.Tensor                 # float32[rows]
+
+
+def _checked(dev: torch.device, name: str, *args):
+    """Calls the library with `dev` as the current device, on its current stream."""
+    fn = getattr(_lib.load(), name)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = fn(*args, _here(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _here(dev))
+    _lib.check(name, st)
+
+
+def int8_quantize_tokens(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> Int8Tensor:
+    """x: bf16 [rows][cols] -> int8 codes and one scale for each row: the operands of int8_scaled_gemm, from activations
+    (a row is a token) or from a weight [N][K] (a row is an output channel). `out` reuses caller buffers."""
+    _dev(x, torch.bfloat16, "x")
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][cols]")
+    rows, cols = x.shape
+    dev = x.device
+    if out is None:
+        out = Int8Tensor(torch.empty((rows, cols), dtype=torch.int8, device=dev),
+                         torch.empty(rows, dtype=torch.float32, device=dev))
+    else:
+        _expect(out.q, (rows, cols), torch.int8, dev, "out.q")
+        _expect(out.scale, (rows,), torch.float32, dev, "out.scale")
+    _checked(dev, "int8_quantize_tokens", x.data_ptr(), rows, cols, out.q.data_ptr(), out.scale.data_ptr())
+    return out
+
+
+def _rows_out(out: Optional[torch.Tensor], rows: int, cols: int, dev) -> torch.Tensor:
+    """A new bf16 [rows][cols], or the caller's: its rows may be further apart."""
+    if out is None:
+        return torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    if out.dtype is not torch.bfloat16 or out.shape != (rows, cols) or out.device != dev or \
+            (rows and cols and (out.stride(1) != 1 and cols > 1 or out.stride(0) < cols and rows > 1)):
+        raise ValueError(f"out must be a bf16 tensor of shape {(rows, cols)} on {dev} with contiguous rows")
+    return out
+
+
+def int8_scaled_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor, b_scale: torch.Tensor,
+                     swiglu: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """bf16 C[M][N] = (A[M][K] B[N][K]^T) a_scale[m] b_scale[n], the sum exact. With swiglu, B holds the N/2 gate rows,
+    then the N/2 up rows, and the result is silu(gate) * up [M][N/2]. `out` may be rows of a wider tensor."""
+    _dev(a_q, torch.int8, "a_q")
+    if a_q.dim() != 2 or b_q.dim() != 2:
+        raise ValueError("a_q must be [M][K], b_q [N][K]")
+    M, K = a_q.shape
+    N = b_q.shape[0]
+    dev = a_q.device
+    _expect(b_q, (N, K), torch.int8, dev, "b_q")
+    _expect(a_scale, (M,), torch.float32, dev, "a_scale")
+    _expect(b_scale, (N,), torch.float32, dev, "b_scale")
+    cols = N // 2 if swiglu else N
+    out = _rows_out(out, M, cols, dev)
+    _checked(dev, "int8_scaled_gemm", a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(), M, N, K,
+             1 if swiglu else 0, out.data_ptr(), out.stride(0) if M > 1 else max(cols, 1))
+    return out
+
+
+def int8_grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, offsets: torch.Tensor, b_q: torch.Tensor,
+                      b_scale: torch.Tensor, swiglu: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """int8_scaled_gemm over expert groups of any number of rows: rows [offsets[g], offsets[g + 1]) (int64[G + 1], on the
+    device) of a_q [rows][K] times b_q [G][N][K]^T with b_scale [G][N]. Rows outside every group are not written."""
+    _dev(a_q, torch.int8, "a_q")
+    if a_q.dim() != 2 or b_q.dim() != 3:
+        raise ValueError("a_q must be [rows][K], b_q [G][N][K]")
+    rows, K = a_q.shape
+    G, N = b_q.shape[:2]
+    dev = a_q.device
+    _expect(b_q, (G, N, K), torch.int8, dev, "b_q")
+    _expect(offsets, (G + 1,), torch.int64, dev, "offsets")
+    _expect(a_scale, (rows,), torch.float32, dev, "a_scale")
+    _expect(b_scale, (G, N), torch.float32, dev, "b_scale")
+    cols = N // 2 if swiglu else N
+    out = _rows_out(out, rows, cols, dev)
+    _checked(dev, "int8_grouped_gemm", a_q.data_ptr(), a_scale.data_ptr(), offsets.data_ptr(), G, rows, b_q.data_ptr(),
+             b_scale.data_ptr(), N, K, 1 if swiglu else 0, out.data_ptr(), out.stride(0) if rows > 1 else max(cols, 1))
+    return out
+
+
+class QKNormGrads(NamedTuple):
+    dqk: torch.Tensor                   # bf16 [tokens][(heads_q + heads_k) * head_dim], or the caller's wider rows
+    dgamma_q: Optional[torch.Tensor]    # float32[head_dim] (None without a norm, or when not wanted)
+    dgamma_k: Optional[torch.Tensor]
+
+
+def _expect_rotation(tokens: int, positions: torch.Tensor, inv_freq: torch.Tensor, pair_axis, gamma_q, gamma_k,
+                     head_dim: int, dev):
+    """Checks what qk_norm_rope and its backward share; returns (axes, rot, pair_axis as bytes)."""
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    _expect(positions, (tokens,) if positions.dim() == 1 else (axes, tokens), torch.int64, dev, "positions")
+    pairs = inv_freq.numel()
+    _expect(inv_freq, (pairs,), torch.float32, dev, "inv_freq")
+    if (gamma_q is None) != (gamma_k is None):
+        raise ValueError("gamma_q and gamma_k go together")
+    if gamma_q is not None:
+        _expect(gamma_q, (head_dim,), torch.float32, dev, "gamma_q")
+        _expect(gamma_k, (head_dim,), torch.float32, dev, "gamma_k")
+    if pair_axis is not None:
+        if len(pair_axis) != pairs:
+            raise ValueError("pair_axis must name one axis for each of inv_freq's pairs")
+        pair_axis = bytes(pair_axis)
+    return axes, 2 * pairs, pair_axis
+
+
+def _expect_heads(t: torch.Tensor, tokens: int, heads: int, head_dim: int, dev, name: str):
+    """A view [tokens][heads][head_dim] of any token and head stride."""
+    if t.dtype is not torch.bfloat16 or t.shape != (tokens, heads, head_dim) or t.device != dev or t.stride(2) != 1:
+        raise ValueError(f"{name} must be a bf16 view of shape {(tokens, heads, head_dim)} on {dev} with contiguous heads")
+
+
+def _expect_rows(t: torch.Tensor, tokens: int, width: int, dev, name: str):
+    """bf16 rows of at least `width` values."""
+    if t.dtype is not torch.bfloat16 or t.dim() != 2 or t.shape[0] != tokens or t.shape[1] < width or t.device != dev or \
+            t.stride(1) != 1:
+        raise ValueError(f"{name} must be bf16 [{tokens}][>= {width}] on {dev} with contiguous rows")
+
+
+def qk_norm_rope(qkv: torch.Tensor, heads_q: int, heads_k: int, head_dim: int, positions: torch.Tensor,
+                 inv_freq: torch.Tensor, gamma_q: Optional[torch.Tensor] = None, gamma_k: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, pair_axis=None, interleaved: bool = False, out=None):
+    """RMSNorm of every query and key head (without gammas: none) and the rotation by position, from a QKV projection's
+    output: qkv bf16 [tokens][>= (heads_q + heads_k) * head_dim], query heads first, then key heads. positions int64
+    [tokens] or [axes][tokens]; inv_freq float32[pairs], turning the first 2 * pairs values of a head; pair_axis names the
+    axis of each pair (a sequence of whole numbers; None: axis 0), e.g. [0] * 16 + [1] * 24 + [2] * 24 for time, height and
+    width; interleaved pairs neighbours instead of halves. Returns (q, k), bf16 [tokens][heads][head_dim]; `out` is such a
+    pair of views of any token and head strides (rows of a cache, head-major tensors, or qkv's own heads)."""
+    width = (heads_q + heads_k) * head_dim
+    if not qkv.is_cuda or qkv.dim() != 2:
+        raise ValueError("qkv must be a device tensor [tokens][>= heads * head_dim]")
+    tokens, dev = qkv.shape[0], qkv.device
+    _expect_rows(qkv, tokens, width, dev, "qkv")
+    axes, rot, pair_axis = _expect_rotation(tokens, positions, inv_freq, pair_axis, gamma_q, gamma_k, head_dim, dev)
+    if out is None:
+        q = torch.empty((tokens, heads_q, head_dim), dtype=torch.bfloat16, device=dev)
+        k = torch.empty((tokens, heads_k, head_dim), dtype=torch.bfloat16, device=dev)
+    else:
+        q, k = out
+        _expect_heads(q, tokens, heads_q, head_dim, dev, "out[0]")
+        _expect_heads(k, tokens, heads_k, head_dim, dev, "out[1]")
+    _checked(dev, "qk_norm_rope", qkv.data_ptr(), qkv.stride(0), tokens, heads_q, heads_k, head_dim, _at(gamma_q),
+             _at(gamma_k), eps, positions.data_ptr(), axes, inv_freq.data_ptr(), rot, pair_axis, 1 if interleaved else 0,
+             q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1))
+    return q, k
+
+
+def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: Optional[torch.Tensor], positions: torch.Tensor,
+                          inv_freq: torch.Tensor, gamma_q: Optional[torch.Tensor] = None,
+                          gamma_k: Optional[torch.Tensor] = None, eps: float = 1e-6, pair_axis=None,
+                          interleaved: bool = False, want_dgamma: bool = True, accumulate=None,
+                          out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> QKNormGrads:
+    """Gradients of qk_norm_rope: dq and dk bf16 [tokens][heads][head_dim] (views of any token and head strides), qkv its
+    input (None without a norm). dqk is bf16 [tokens][(heads_q + heads_k) * head_dim]; `out` may hold wider rows, whose
+    further columns are left as they were, or be qkv itself. dgamma_q and dgamma_k are new float32[head_dim], or are added
+    into the pair `accumulate`; None without a norm or with want_dgamma=False."""
+    if not dq.is_cuda or dq.dim() != 3 or dk.dim() != 3:
+        raise ValueError("dq and dk must be device tensors [tokens][heads][head_dim]")
+    tokens, heads_q, head_dim = dq.shape
+    heads_k, dev = dk.shape[1], dq.device
+    width = (heads_q + heads_k) * head_dim
+    _expect_heads(dq, tokens, heads_q, head_dim, dev, "dq")
+    _expect_heads(dk, tokens, heads_k, head_dim, dev, "dk")
+    axes, rot, pair_axis = _expect_rotation(tokens, positions, inv_freq, pair_axis, gamma_q, gamma_k, head_dim, dev)
+    if gamma_q is None:
+        qkv, ld = None, width
+    else:
+        if qkv is None:
+            raise ValueError("qkv is needed with a norm")
+        _expect_rows(qkv, tokens, width, dev, "qkv")
+        ld = qkv.stride(0)
+    if out is None:
+        out = torch.empty((tokens, width), dtype=torch.bfloat16, device=dev)
+    else:
+        _expect_rows(out, tokens, width, dev, "out")
+    gq = gk = None
+    if gamma_q is not None and accumulate is not None:
+        gq, gk = accumulate
+        _expect(gq, (head_dim,), torch.float32, dev, "accumulate[0]")
+        _expect(gk, (head_dim,), torch.float32, dev, "accumulate[1]")
+    elif gamma_q is not None and want_dgamma:
+        gq = torch.empty(head_dim, dtype=torch.float32, device=dev)
+        gk = torch.empty(head_dim, dtype=torch.float32, device=dev)
+    if gq is not None and workspace is None:
+        workspace = torch.empty(workspace_bytes("qk_norm_backward", head_dim), dtype=torch.uint8, device=dev)
+    _checked(dev, "qk_norm_rope_backward", dq.data_ptr(), dq.stride(0), dq.stride(1), dk.data_ptr(), dk.stride(0),
+             dk.stride(1), _at(qkv), ld, tokens, heads_q, heads_k, head_dim, _at(gamma_q), _at(gamma_k), eps,
+             positions.data_ptr(), axes, inv_freq.data_ptr(), rot, pair_axis, 1 if interleaved else 0, out.data_ptr(),
+             out.stride(0), _at(gq), _at(gk), 1 if accumulate is not None else 0, _at(workspace),
+             0 if workspace is None else _scratch(workspace, dev))
+    return QKNormGrads(out, gq, gk)

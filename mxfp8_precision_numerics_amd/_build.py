@@ -15,7 +15,7 @@ PROBE_LIB = os.path.join(PKG, "libmxq_probe.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["quantize.hip", "gemm.hip", "adam.hip", "gradcomm.hip", "moe.hip", "norm.hip", "checkpoint.hip",
-           "moe_few.hip", "abi.hip"]
+           "moe_few.hip", "int8.hip", "qk_norm.hip", "abi.hip"]
 PROBE_SOURCES = ["probe.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -57,6 +57,13 @@ SIGNATURES = {
     "swiglu_backward_mx_checkpoint": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _P, _P, _P, _P, _I, _P]),
     "moe_mx_few_tokens": (_I, [_P, _P, _P, _I64, _I64, _I64, _I, _P, _P, _P, _P, _I64, _I64, _P, _P, _SZ, _P]),
     "moe_mx_few_tokens_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "int8_quantize_tokens": (_I, [_P, _I64, _I64, _P, _P, _P]),
+    "int8_scaled_gemm": (_I, [_P, _P, _P, _P, _I64, _I64, _I64, _I, _P, _I64, _P]),
+    "int8_grouped_gemm": (_I, [_P, _P, _P, _I64, _I64, _P, _P, _I64, _I64, _I, _P, _I64, _P]),
+    "qk_norm_rope": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _P, _P, _F, _P, _I64, _P, _I64, C.c_char_p, _I, _P, _I64, _I64,
+                          _P, _I64, _I64, _P]),
+    "qk_norm_rope_backward": (_I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _I64, _I64, _P, _P, _F, _P, _I64,
+                                   _P, _I64, C.c_char_p, _I, _P, _I64, _P, _P, _I, _P, _SZ, _P]),
     "grouped_wgrad_mx": (_I, [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P]),
 }
 

@@ -18,10 +18,59 @@ size_t pertensor_ws(int64_t n) { return round_up((size_t)mxq::pertensor_amax_par
 size_t adam_ws(int64_t n) { return round_up((size_t)mxq::adam_parts(n) * 4u, 256) + 256; }
 // One partial row of dgamma (cols floats) per workgroup of the backward.
 size_t rmsnorm_backward_ws(int64_t cols) { return round_up((size_t)mxq::kNormBwdParts * (size_t)cols * 4u, 256); }
+// One row of the dgamma sums of queries and keys (2 dim floats) per workgroup of the backward.
+size_t qk_norm_backward_ws(int64_t dim) {
+    return dim > mxq::kQkMaxDim ? 0 : round_up((size_t)mxq::kQkBwdParts * 2u * (size_t)dim * 4u, 256);
+}
 constexpr size_t kDelayedWs = 256;   // delayed modes: the atomic amax word (and Adam's three constants)
 constexpr int64_t kMaxHistory = 1 << 20;
 
 constexpr int64_t kMaxGridY = 65535;
+
+// A stride between `count` pieces of at least `least` elements, 16-byte aligned; with fewer than two pieces it is not used.
+bool stride_ok(int64_t stride, int64_t count, int64_t least) {
+    return count < 2 || (stride >= least && stride % 8 == 0 && stride <= INT64_MAX / 2 / count);
+}
+
+// The checks that qk_norm_rope and its backward share, and the arguments of their kernels.
+mxq_status qk_args(const uint16_t* x, int64_t ld, int64_t tokens, int64_t hq, int64_t hk, int64_t dim, const float* gamma_q,
+                   const float* gamma_k, float eps, const int64_t* positions, int64_t axes, const float* inv_freq,
+                   int64_t rot, const uint8_t* pair_axis, int interleaved, uint16_t* q, int64_t q_token, int64_t q_head,
+                   uint16_t* k, int64_t k_token, int64_t k_head, mxq::QkArgs& a) {
+    if ((gamma_q == nullptr) != (gamma_k == nullptr)) return MXQ_ERR_NULL;
+    if (gamma_q && !(eps > 0.0f && eps < 3.0e38f)) return MXQ_ERR_UNSUPPORTED;                  // NaN fails too
+    if (tokens < 0 || tokens > (int64_t(1) << 25) || hq < 0 || hk < 0 || hq > 65536 || hk > 65536) return MXQ_ERR_SHAPE;
+    if (dim < 16 || dim > mxq::kQkMaxDim || dim % 16 != 0 || rot < 0 || rot > dim || rot % 16 != 0) return MXQ_ERR_SHAPE;
+    if (axes < 1 || axes > mxq::kQkMaxAxes) return MXQ_ERR_SHAPE;
+    a = mxq::QkArgs{};
+    for (int64_t i = 0; pair_axis && i < rot / 2; ++i) {
+        if (pair_axis[i] >= axes) return MXQ_ERR_SHAPE;
+        a.axis[i >> 4] |= (uint32_t)pair_axis[i] << (2 * (i & 15));
+    }
+    if (!stride_ok(ld, tokens, (hq + hk) * dim) || !stride_ok(q_token, hq ? tokens : 0, dim) ||
+        !stride_ok(q_head, tokens ? hq : 0, dim) || !stride_ok(k_token, hk ? tokens : 0, dim) ||
+        !stride_ok(k_head, tokens ? hk : 0, dim))
+        return MXQ_ERR_SHAPE;
+    if (tokens > 0 && hq + hk > 0) {
+        if ((hq && !q) || (hk && !k) || (rot && (!positions || !inv_freq))) return MXQ_ERR_NULL;
+        if (!al16(x) || !al16(gamma_q) || !al16(gamma_k) || !al16(q) || !al16(k)) return MXQ_ERR_ALIGN;
+        if ((reinterpret_cast<uintptr_t>(positions) & 7u) || !al4(inv_freq)) return MXQ_ERR_ALIGN;
+    }
+    a.x = x; a.ldx = ld; a.tokens = tokens; a.gamma_q = gamma_q; a.gamma_k = gamma_k; a.positions = positions;
+    a.inv_freq = inv_freq; a.q = q; a.k = k; a.q_token = q_token; a.q_head = q_head; a.k_token = k_token; a.k_head = k_head;
+    a.eps = eps; a.hq = (int)hq; a.hk = (int)hk; a.dim = (int)dim; a.rot = (int)rot; a.interleaved = interleaved != 0;
+    return MXQ_OK;
+}
+
+// Shapes of the int8 products: rows of A, rows and columns of B, and the output's columns and row stride.
+mxq_status int8_gemm_shape(int64_t M, int64_t N, int64_t K, int64_t G, int swiglu, int64_t ldc) {
+    if (M < 0 || N < 0 || K < 32 || K % 32 != 0 || K >= 131072 || (swiglu && N % 2 != 0)) return MXQ_ERR_SHAPE;
+    const int64_t cols = swiglu ? N / 2 : N;
+    if (ldc < cols) return MXQ_ERR_SHAPE;
+    if (M > (int64_t(1) << 40) || N > (int64_t(1) << 30) || ldc > (int64_t(1) << 40)) return MXQ_ERR_SHAPE;
+    if (M && cols && mxq::int8_gemm_blocks(M, cols, G, swiglu) > mxq::kMaxThreads / 256) return MXQ_ERR_SHAPE;
+    return MXQ_OK;
+}
 
 // Adam's moment decay rates lie in [0, 1): the bias corrections divide by 1 - beta^t. NaN fails both comparisons.
 bool betas_ok(const mxq_adam_hparams& hp) {
@@ -78,6 +127,7 @@ size_t mxq_workspace_bytes(const char* op, int64_t n) {
     if (strcmp(op, "pertensor") == 0) return pertensor_ws(n);
     if (strcmp(op, "adam") == 0) return adam_ws(n);
     if (strcmp(op, "rmsnorm_backward") == 0) return rmsnorm_backward_ws(n);
+    if (strcmp(op, "qk_norm_backward") == 0) return qk_norm_backward_ws(n);
     if (strcmp(op, "pertensor_delayed") == 0 || strcmp(op, "adam_delayed") == 0 || strcmp(op, "autoscale") == 0)
         return kDelayedWs;
     return 0;
@@ -540,6 +590,90 @@ mxq_status moe_mx_few_tokens(const uint8_t* x_q, const uint8_t* x_s, const float
     if (!al16(workspace)) return MXQ_ERR_ALIGN;
     return hip_status(mxq::launch_moe_few(x_q, x_s, logits, w_up_q, w_up_s, w_down_q, w_down_s, tokens, experts, topk,
                                           D, F, normalize ? 1 : 0, y_bf16, workspace, stream));
+}
+
+mxq_status int8_quantize_tokens(const uint16_t* x_bf16, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                                hipStream_t stream) {
+    if (rows < 0 || cols < 0 || cols % 32 != 0) return MXQ_ERR_SHAPE;
+    if (rows > mxq::int8_quantize_max_rows(cols)) return MXQ_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return MXQ_OK;
+    if (!x_bf16 || !q || !scale) return MXQ_ERR_NULL;
+    if (!al16(x_bf16) || !al16(q) || !al4(scale)) return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_int8_quantize(x_bf16, rows, cols, q, scale, stream));
+}
+
+mxq_status int8_scaled_gemm(const int8_t* a_q, const float* a_scale, const int8_t* b_q, const float* b_scale, int64_t M,
+                            int64_t N, int64_t K, int swiglu, uint16_t* c_bf16, int64_t ldc, hipStream_t stream) {
+    const mxq_status shape = int8_gemm_shape(M, N, K, 0, swiglu, ldc);
+    if (shape != MXQ_OK) return shape;
+    if (M == 0 || N == 0) return MXQ_OK;
+    if (!a_q || !a_scale || !b_q || !b_scale || !c_bf16) return MXQ_ERR_NULL;
+    if (!al16(a_q) || !al16(b_q) || !al4(a_scale) || !al4(b_scale) || (reinterpret_cast<uintptr_t>(c_bf16) & 1u))
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_int8_gemm(a_q, a_scale, nullptr, 0, M, b_q, b_scale, N, K, swiglu != 0, c_bf16, ldc,
+                                            stream));
+}
+
+mxq_status int8_grouped_gemm(const int8_t* a_q, const float* a_scale, const int64_t* group_offsets, int64_t G,
+                             int64_t total_rows, const int8_t* b_q, const float* b_scale, int64_t N, int64_t K, int swiglu,
+                             uint16_t* c_bf16, int64_t ldc, hipStream_t stream) {
+    if (G < 1 || G > 4096) return MXQ_ERR_SHAPE;
+    const mxq_status shape = int8_gemm_shape(total_rows, N, K, G, swiglu, ldc);
+    if (shape != MXQ_OK) return shape;
+    if (total_rows == 0 || N == 0) return MXQ_OK;
+    if (!a_q || !a_scale || !group_offsets || !b_q || !b_scale || !c_bf16) return MXQ_ERR_NULL;
+    if (!al16(a_q) || !al16(b_q) || !al4(a_scale) || !al4(b_scale) || !al16(group_offsets) ||
+        (reinterpret_cast<uintptr_t>(c_bf16) & 1u))
+        return MXQ_ERR_ALIGN;
+    return hip_status(mxq::launch_int8_gemm(a_q, a_scale, group_offsets, G, total_rows, b_q, b_scale, N, K, swiglu != 0,
+                                            c_bf16, ldc, stream));
+}
+
+mxq_status qk_norm_rope(const uint16_t* qkv_bf16, int64_t ld, int64_t tokens, int64_t heads_q, int64_t heads_k,
+                        int64_t head_dim, const float* gamma_q, const float* gamma_k, float eps, const int64_t* positions,
+                        int64_t axes, const float* inv_freq, int64_t rot, const uint8_t* pair_axis, int interleaved,
+                        uint16_t* q_bf16, int64_t q_token_stride, int64_t q_head_stride, uint16_t* k_bf16,
+                        int64_t k_token_stride, int64_t k_head_stride, hipStream_t stream) {
+    mxq::QkArgs a;
+    const mxq_status st = qk_args(qkv_bf16, ld, tokens, heads_q, heads_k, head_dim, gamma_q, gamma_k, eps, positions, axes,
+                                  inv_freq, rot, pair_axis, interleaved, q_bf16, q_token_stride, q_head_stride, k_bf16,
+                                  k_token_stride, k_head_stride, a);
+    if (st != MXQ_OK) return st;
+    if (tokens == 0 || heads_q + heads_k == 0) return MXQ_OK;
+    if (!qkv_bf16) return MXQ_ERR_NULL;
+    return hip_status(mxq::launch_qk_forward(a, stream));
+}
+
+mxq_status qk_norm_rope_backward(const uint16_t* dq_bf16, int64_t dq_token_stride, int64_t dq_head_stride,
+                                 const uint16_t* dk_bf16, int64_t dk_token_stride, int64_t dk_head_stride,
+                                 const uint16_t* qkv_bf16, int64_t ld, int64_t tokens, int64_t heads_q, int64_t heads_k,
+                                 int64_t head_dim, const float* gamma_q, const float* gamma_k, float eps,
+                                 const int64_t* positions, int64_t axes, const float* inv_freq, int64_t rot,
+                                 const uint8_t* pair_axis, int interleaved, uint16_t* dqkv_bf16, int64_t ld_d,
+                                 float* dgamma_q, float* dgamma_k, int accumulate, void* workspace, size_t workspace_bytes,
+                                 hipStream_t stream) {
+    mxq::QkArgs a;
+    // without a norm the input is not read, nor its stride
+    const mxq_status st = qk_args(qkv_bf16, gamma_q ? ld : (heads_q + heads_k) * head_dim, tokens, heads_q, heads_k,
+                                  head_dim, gamma_q, gamma_k, eps, positions, axes, inv_freq, rot, pair_axis, interleaved,
+                                  const_cast<uint16_t*>(dq_bf16), dq_token_stride, dq_head_stride,
+                                  const_cast<uint16_t*>(dk_bf16), dk_token_stride, dk_head_stride, a);
+    if (st != MXQ_OK) return st;
+    if ((dgamma_q == nullptr) != (dgamma_k == nullptr)) return MXQ_ERR_NULL;
+    if (dgamma_q && !gamma_q) return MXQ_ERR_UNSUPPORTED;
+    if (!stride_ok(ld_d, tokens, (heads_q + heads_k) * head_dim)) return MXQ_ERR_SHAPE;
+    const bool empty = tokens == 0 || heads_q + heads_k == 0;
+    if (empty && !dgamma_q) return MXQ_OK;
+    if (!empty && (!dqkv_bf16 || (gamma_q && !qkv_bf16))) return MXQ_ERR_NULL;
+    if (!al16(dqkv_bf16) || !al16(dgamma_q) || !al16(dgamma_k)) return MXQ_ERR_ALIGN;
+    if (dgamma_q) {
+        if (!workspace || workspace_bytes < qk_norm_backward_ws(head_dim)) return MXQ_ERR_WORKSPACE;
+        if (!al16(workspace)) return MXQ_ERR_ALIGN;
+    }
+    a.dx = dqkv_bf16;
+    a.lddx = ld_d;
+    a.partial = dgamma_q ? static_cast<float*>(workspace) : nullptr;
+    return hip_status(mxq::launch_qk_backward(a, dgamma_q, dgamma_k, accumulate ? 1 : 0, stream));
 }
 
 }  // extern "C"

@@ -27,7 +27,7 @@
 // distinct banks. The large-tile kernel (gemm_big_kernel) is described where it is defined.
 #include <type_traits>
 
-#include "mxq_device.h"
+#include "gemm_tile.h"
 #include "launch.h"
 
 namespace mxq {
@@ -69,7 +69,6 @@ __device__ __forceinline__ int swz(int row, int chunk) { return row * BK + ((chu
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf_t __attribute__((ext_vector_type(2)));
-typedef int v4i __attribute__((ext_vector_type(4)));
 
 // 8 FP8 codes (E4M3 when FMT == 0, E5M2 when 1) -> 8 bf16 equal to code * 2^E, where E is the exponent field of
 // `scale` (exact whenever the product is representable in bf16).
@@ -88,50 +87,6 @@ __device__ __forceinline__ v8bf dequant8_bf16(uint2 x, float scale) {
         p3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((int)x.y, scale, true);
     }
     return v8bf{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
-}
-
-// Row-grouped GEMMs: the expert group that holds row tile t (tiles of TH rows, numbered group by group, each group's
-// rows [off[q], off[q+1]) clamped to [0, M) and cut into ceil(rows / TH) tiles). Each wave scans 64 groups at a time:
-// lane l loads group base + l's offsets, a wave prefix sum of the tile counts finds the group, so a workgroup pays one
-// round of loads per 64 groups instead of a dependent load per group. grp = -1 when t lies past the last tile.
-struct RowTile {
-    int64_t grp, lo, hi;      // group, first row of the tile, end of the group's rows
-};
-
-template <int TH>
-__device__ __forceinline__ RowTile find_row_tile(const GemmArgs& g, int64_t t) {
-    const int lane = threadIdx.x & 63;
-    RowTile r{-1, 0, 0};
-    int64_t before = 0;                          // tiles of the groups already scanned
-    for (int64_t base = 0; base < g.G; base += 64) {
-        const int64_t q = base + lane;
-        int64_t a0 = 0, a1 = 0;
-        int nt = 0;
-        if (q < g.G) {
-            a0 = g.offsets[q];
-            a1 = g.offsets[q + 1];
-            a0 = a0 < 0 ? 0 : (a0 > g.M ? g.M : a0);
-            a1 = a1 < a0 ? a0 : (a1 > g.M ? g.M : a1);
-            nt = (int)((a1 - a0 + TH - 1) / TH);
-        }
-        int incl = nt;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(incl, off, 64);
-            if (lane >= off) incl += v;
-        }
-        const uint64_t hit = __ballot(before + incl > t);
-        if (hit) {
-            const int L = __ffsll((unsigned long long)hit) - 1;
-            const int64_t excl = before + __shfl(incl - nt, L, 64);
-            r.grp = base + L;
-            r.lo = __shfl(a0, L, 64) + (t - excl) * TH;
-            r.hi = __shfl(a1, L, 64);
-            return r;
-        }
-        before += __shfl(incl, 63, 64);
-    }
-    return r;
 }
 
 template <bool MX, int FA, int FB, int GM, int MF>
@@ -159,7 +114,7 @@ __global__ __launch_bounds__(GTHREADS) void gemm_kernel(GemmArgs g) {
         const int64_t bid = blockIdx.x;
         const int64_t t = bid / tiles_n;
         n0 = (bid % tiles_n) * BN;
-        const RowTile rt = find_row_tile<BM>(g, t);
+        const RowTile rt = find_row_tile<BM>(g.offsets, g.G, g.M, t);
         const int64_t grp = rt.grp, lo = rt.lo, hi = rt.hi;
         if (grp < 0) return;                          // more workgroups than tiles: nothing to do
         m0 = lo;
@@ -424,46 +379,6 @@ constexpr int kCopySlot[8] = {1, 3, 5, 7, 9, 11, 13, 15};
 
 __device__ __forceinline__ int swz8(int row) { return (row >> 2) & 3; }
 
-// Raw buffer resource (base, stride 0, 2^31 - 1 bytes, raw untyped access) for a workgroup-uniform address. The
-// address is moved to scalar registers explicitly: values derived from the tile index are computed with vector
-// instructions, and the descriptor must live in scalar registers.
-// With `records` set, accesses at or past that many bytes from the base are out of range: loads return zero and
-// nothing outside the buffer is touched.
-__device__ __forceinline__ v4i buffer_rsrc(const void* p, uint32_t records = 0x7FFFFFFFu) {
-    const uint64_t a = reinterpret_cast<uint64_t>(p);
-    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-    return v4i{(int)lo, (int)(hi & 0xFFFFu), (int)__builtin_amdgcn_readfirstlane(records), 0x00020000};
-}
-
-// LDS offset (the low 32 bits of a shared-aperture address) of an LDS location, made wave-uniform.
-__device__ __forceinline__ uint32_t lds_offset(const void* p) {
-    return __builtin_amdgcn_readfirstlane((uint32_t)reinterpret_cast<uintptr_t>(p));
-}
-
-// Asynchronous copy global -> LDS: each lane reads BYTES (16 or 4) at base + voff + soff and the wave's results land
-// in consecutive slots starting at LDS offset `lds` (M0). Written as inline assembly on purpose: the compiler does
-// not then treat the copy as an LDS write, so LDS reads of other stages are not made to wait for it. The kernel
-// orders copies itself (wait_copies_barrier): a stage is read only after its copies have completed on every wave,
-// and a buffer is refilled only after every wave has finished reading it.
-template <int BYTES>
-__device__ __forceinline__ void dma_to_lds(v4i rsrc, uint32_t lds, int voff, int soff) {
-    if constexpr (BYTES == 16)
-        asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds"
-                     :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
-    else
-        asm volatile("buffer_load_dword %0, %1, %2 offen lds"
-                     :: "v"(voff), "s"(rsrc), "s"(soff), "{m0}"(lds) : "memory");
-}
-
-// Wait until at most N of this wave's copies are still outstanding (vector-memory counter, which retires in issue
-// order) and all its LDS reads have returned, then join the workgroup barrier. One asm statement with a memory
-// clobber, so the compiler keeps LDS accesses on their side of it.
-template <int N>
-__device__ __forceinline__ void wait_copies_barrier() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
-}
-
 // One output tile (workgroup-uniform index bid) of the large-tile kernel; returning ends the tile.
 template <bool MX, int FA, int FB, int GM, int MF>
 __device__ __forceinline__ void gemm_big_tile(const GemmArgs& g, const int bid_in) {
@@ -528,7 +443,7 @@ __device__ __forceinline__ void gemm_big_tile(const GemmArgs& g, const int bid_i
                                 : b;
         const int64_t t = bid / tiles_n;
         n0 = (bid % tiles_n) * TB;
-        const RowTile rt = find_row_tile<TB>(g, t);
+        const RowTile rt = find_row_tile<TB>(g.offsets, g.G, g.M, t);
         const int64_t grp = rt.grp, lo = rt.lo, hi = rt.hi;
         if (grp < 0) return;
         m0 = lo;

@@ -107,4 +107,37 @@ hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* l
                           int64_t k, int64_t D, int64_t F, int normalize, uint16_t* y, void* workspace,
                           hipStream_t stream);
 
+// 8-bit integer operands (int8.hip). G = 0: dense; offsets then NULL.
+int64_t int8_quantize_max_rows(int64_t cols);   // of one launch
+hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
+                                hipStream_t stream);
+int64_t int8_gemm_blocks(int64_t M, int64_t cols, int64_t G, int swiglu);   // workgroups of the largest grid a call uses
+hipError_t launch_int8_gemm(const int8_t* a_q, const float* a_scale, const int64_t* offsets, int64_t G, int64_t M,
+                            const int8_t* b_q, const float* b_scale, int64_t N, int64_t K, int swiglu, uint16_t* c,
+                            int64_t ldc, hipStream_t stream);
+
+// Head norms with the rotation by position (qk_norm.hip). In the backward q and k are the gradients of the outputs.
+constexpr int64_t kQkMaxDim = 256;
+constexpr int64_t kQkMaxAxes = 4;
+constexpr int64_t kQkBwdParts = 1024;
+struct QkArgs {
+    const uint16_t* x;                      // [tokens][ldx]: hq query heads, then hk key heads, of dim values
+    int64_t ldx, tokens;
+    const float *gamma_q, *gamma_k;         // NULL: no norm
+    const int64_t* positions;               // [axes][tokens]
+    const float* inv_freq;                  // [rot / 2]
+    uint16_t *q, *k;
+    int64_t q_token, q_head, k_token, k_head;
+    uint16_t* dx;                           // backward: [tokens][lddx], laid out like x
+    int64_t lddx;
+    float* partial;                         // backward: a row of 2 dim sums for each workgroup
+    float eps, inv_dim;                     // inv_dim: set by the launchers, as the last five are
+    int hq, hk, dim, rot, interleaved;
+    uint32_t axis[8];                       // 2 bits a pair
+    int q_blocks, k_blocks, splits, per_item;
+    int64_t items;
+};
+hipError_t launch_qk_forward(QkArgs a, hipStream_t stream);
+hipError_t launch_qk_backward(QkArgs a, float* dgamma_q, float* dgamma_k, int accumulate, hipStream_t stream);
+
 }  // namespace mxq

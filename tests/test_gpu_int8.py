@@ -1,0 +1,243 @@
+"""The int8 operators against 64-bit arithmetic. Codes and integer sums are exact, so codes have to be equal and a plain
+product is the one fp32 sequence the interface names, bit for bit."""
+import pytest
+import torch
+
+import mxfp8_precision_numerics_amd as mxq
+from gpu_util import DEV, need_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+
+def _gen(seed):
+    need_gpu()
+    return torch.Generator(device=DEV).manual_seed(seed)
+
+
+# ------------------------------------------------------------------------------------------------ quantization
+def _expected(x):
+    """Codes and scales by the definition in 64 bits (whole bf16 significands: the quotient is exact enough to round)."""
+    v = x.double()
+    amax = v.abs().amax(1)
+    bad = ~torch.isfinite(amax)
+    q = torch.round(127.0 * v / torch.where(amax == 0, torch.ones_like(amax), amax)[:, None])
+    q[bad] = 0
+    scale = (amax / 127.0).float()        # the fp32 quotient, to nearest (an 8-bit number over 127 is never near a tie)
+    scale[bad] = float("nan")
+    return q.to(torch.int8), scale
+
+
+def _same_scale(a, b):
+    return torch.equal(torch.nan_to_num(a, nan=-1.0), torch.nan_to_num(b, nan=-1.0))
+
+
+@pytest.mark.parametrize("rows,cols", [(1, 32), (1, 2048), (3, 512), (5, 544), (7, 1056), (6, 2080), (33, 8192), (9, 8224),
+                                       (4, 12288), (3, 32768), (2, 32800), (3, 49152), (257, 96)])
+def test_quantize(rows, cols):
+    g = _gen(rows * 7919 + cols)
+    x = (torch.randn(rows, cols, generator=g, device=DEV) *
+         torch.exp2(torch.randint(-20, 20, (rows, 1), generator=g, device=DEV).float())).bfloat16()
+    say("int8_quantize_tokens", rows, cols)
+    r = mxq.int8_quantize_tokens(x)
+    q, s = _expected(x)
+    assert torch.equal(r.q, q) and torch.equal(r.scale, s)
+
+
+def test_quantize_every_pair_of_significands():
+    """Every ratio of an 8-bit significand to a row's largest, 10 binades down: all halves between two codes are among
+    them (254, say, is the largest of 127.5's neighbours)."""
+    need_gpu()
+    top = torch.arange(128, 256, device=DEV).float()                      # a row for each largest significand
+    vals = (torch.arange(128, 256, device=DEV).float()[None] * torch.exp2(-torch.arange(0, 10, device=DEV).float())[:, None])
+    x = torch.minimum(vals.reshape(1, -1).expand(128, -1), top[:, None]).clone()
+    x[:, ::2] *= -1
+    x = torch.cat([x, top[:, None].expand(-1, 32)], 1)
+    for e in (0, -100, 60):
+        y = (x * 2.0 ** e).bfloat16()
+        r = mxq.int8_quantize_tokens(y)
+        q, s = _expected(y)
+        assert torch.equal(r.q, q) and torch.equal(r.scale, s)
+
+
+@pytest.mark.parametrize("cols", [64, 4096, 16384, 40960])
+def test_quantize_special_rows(cols):
+    g = _gen(cols)
+    x = torch.randn(10, cols, generator=g, device=DEV).bfloat16()
+    x[1] = 0
+    x[2, cols // 2] = float("nan")
+    x[3, 5] = float("inf")
+    x[4, cols - 1] = -float("inf")
+    x[5] = 0
+    x[5, 7] = 2.0 ** -133                                                 # the smallest bf16
+    x[6] = x[6].float().mul(2.0 ** -130).bfloat16()                       # subnormal values
+    x[7] = x[7].float().clamp(-3, 3).mul(2.0 ** 126).bfloat16()           # near the largest
+    x[8] = -0.0
+    r = mxq.int8_quantize_tokens(x)
+    q, s = _expected(x)
+    assert torch.equal(r.q, q) and _same_scale(r.scale, s)
+    out = mxq.Int8Tensor(torch.full_like(r.q, 99), torch.full_like(r.scale, 99.0))
+    assert mxq.int8_quantize_tokens(x, out=out) is out and torch.equal(out.q, q) and _same_scale(out.scale, s)
+    assert mxq.int8_quantize_tokens(x[:0]).q.shape == (0, cols)
+
+
+# ------------------------------------------------------------------------------------------------ products
+def _operands(g, M, N, K, groups=None):
+    c = lambda *s: torch.randint(-128, 128, s, generator=g, device=DEV, dtype=torch.int32).to(torch.int8)  # noqa: E731
+    sc = lambda *s: torch.rand(s, generator=g, device=DEV) * 0.02 + 1e-4  # noqa: E731
+    lead = () if groups is None else (groups,)
+    return c(M, K), sc(M), c(*lead, N, K), sc(*lead, N)
+
+
+def _sums(a, b):
+    """Exact integer sums, in 64-bit floating point on the GPU (every partial sum is a whole number below 2^53)."""
+    return a.double() @ b.double().t()
+
+
+def _value(s, sa, sb):
+    return (s.float() * sa[:, None]) * sb[None]                           # fp32, in the order the interface names
+
+
+def _check(c, s, sa, sb, swiglu):
+    if not swiglu:
+        assert torch.equal(c, _value(s, sa, sb).bfloat16())
+        return
+    # g and u are within 3 roundings of 2^-24 of their values; silu passes g's on (1 + |g|)-fold, its exponential and
+    # quotient add at most 12 more, the product one; then the result's rounding to bf16 (2^-8).
+    y = s.double() * sa.double()[:, None] * sb.double()[None]
+    F = y.shape[1] // 2
+    gate, up = y[:, :F], y[:, F:]
+    h = gate / (1.0 + torch.exp(-gate)) * up
+    tol = h.abs() * (2.0 ** -8 + (20.0 + 4.0 * gate.abs()) * 2.0 ** -24) + 1e-30
+    assert bool(((c.double() - h).abs() <= tol).all())
+
+
+SHAPES = [(1, 1, 32), (1, 6144, 2048), (2, 33, 96), (5, 130, 64), (16, 128, 1024), (17, 257, 160), (61, 1000, 544),
+          (64, 256, 4096), (65, 96, 2080), (128, 384, 512), (130, 66, 12288), (200, 5000, 288), (257, 640, 1056),
+          (512, 512, 512), (700, 770, 1504), (1030, 1290, 2048), (1, 514, 36864), (300, 2050, 32)]
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_dense(M, N, K, swiglu):
+    if swiglu:
+        N += N % 2
+    g = _gen(M * 31 + N * 7 + K)
+    a, sa, b, sb = _operands(g, M, N, K)
+    if swiglu:
+        sa = sa * 0.001                                                   # gates of a few units
+    say("int8_scaled_gemm", M, N, K, swiglu)
+    _check(mxq.int8_scaled_gemm(a, sa, b, sb, swiglu=swiglu), _sums(a, b), sa, sb, swiglu)
+
+
+def test_largest_sums():
+    """-128 times -128 over the longest contraction: the sum just fits 32 bits."""
+    need_gpu()
+    K = 131072 - 32
+    a = torch.full((3, K), -128, dtype=torch.int8, device=DEV)
+    b = torch.full((40, K), -128, dtype=torch.int8, device=DEV)
+    b[1::2] = 127
+    sa, sb = torch.full((3,), 1e-3, device=DEV), torch.full((40,), 1e-3, device=DEV)
+    _check(mxq.int8_scaled_gemm(a, sa, b, sb), _sums(a, b), sa, sb, False)
+
+
+@pytest.mark.parametrize("M,N,K,pad", [(3, 100, 64, 1), (130, 257, 512, 7), (600, 1030, 1024, 2)])
+def test_rows_of_a_wider_tensor(M, N, K, pad):
+    g = _gen(M + N)
+    a, sa, b, sb = _operands(g, M, N, K)
+    wide = torch.full((M, N + pad), 7.0, dtype=torch.bfloat16, device=DEV)
+    c = mxq.int8_scaled_gemm(a, sa, b, sb, out=wide[:, :N])
+    _check(c, _sums(a, b), sa, sb, False)
+    assert bool((wide[:, N:] == 7.0).all())
+    odd = torch.full((M * N + 1,), 7.0, dtype=torch.bfloat16, device=DEV)     # rows at odd addresses
+    c = mxq.int8_scaled_gemm(a, sa, b, sb, out=odd[1:].view(M, N))
+    _check(c, _sums(a, b), sa, sb, False)
+    assert float(odd[0]) == 7.0
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_nan_and_zero_scales(M):
+    """A row whose scale is NaN (a quantized row with a NaN) is NaN, one whose scale is 0 is zero, the others as ever."""
+    g = _gen(M)
+    a, sa, b, sb = _operands(g, M, 160, 256)
+    sa[0] = float("nan")
+    if M > 1:
+        sa[M // 2] = 0.0
+    c = mxq.int8_scaled_gemm(a, sa, b, sb)
+    assert bool(torch.isnan(c[0]).all())
+    want = _value(_sums(a, b), sa, sb).bfloat16()
+    assert torch.equal(c[1:], want[1:])
+
+
+GROUPS = [
+    (4, 96, 160, [0, 3, 3, 70, 71]),                                      # an empty expert, odd starts
+    (8, 128, 64, [0, 0, 0, 5, 5, 5, 5, 5, 5]),                            # nearly all empty
+    (3, 257, 544, [0, 1, 130, 300]),
+    (64, 64, 256, None),                                                  # about two rows an expert
+    (5, 770, 1024, [10, 200, 200, 461, 900, 1000]),                       # rows ahead of the first and behind the last
+    (2, 1030, 2048, [0, 700, 1500]),
+    (70, 40, 96, None),
+    (1, 300, 96, [0, 33]),
+]
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("case", range(len(GROUPS)))
+def test_grouped(case, swiglu):
+    G, N, K, off = GROUPS[case]
+    N += N % 2 if swiglu else 0
+    g = _gen(case)
+    if off is None:
+        off = [0] + torch.cumsum(torch.randint(0, 5, (G,), generator=g, device=DEV), 0).tolist()
+    rows = off[-1] + (17 if case in (3, 4) else 0)
+    a, sa, b, sb = _operands(g, rows, N, K, G)
+    if swiglu:
+        sa = sa * 0.001
+    cols = N // 2 if swiglu else N
+    out = torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device=DEV)
+    say("int8_grouped_gemm", G, rows, N, K, swiglu)
+    c = mxq.int8_grouped_gemm(a, sa, torch.tensor(off, device=DEV), b, sb, swiglu=swiglu, out=out)
+    for e in range(G):
+        lo, hi = off[e], off[e + 1]
+        if lo < hi:
+            _check(c[lo:hi], _sums(a[lo:hi], b[e]), sa[lo:hi], sb[e], swiglu)
+    assert bool((c[:off[0]] == 7.0).all()) and bool((c[off[-1]:] == 7.0).all())
+
+
+@pytest.mark.parametrize("off", [[0, 50, 20, 300, 40], [-7, 10, 30, 90, 1 << 40], [100, 90, 80, 70, 60]])
+def test_offsets_that_break_the_rule_write_nothing_astray(off):
+    g = _gen(1)
+    rows, N, K = 128, 96, 64
+    a, sa, b, sb = _operands(g, rows, N, K, 4)
+    whole = torch.full((rows + 64, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    mxq.int8_grouped_gemm(a, sa, torch.tensor(off, device=DEV), b, sb, out=whole[32:32 + rows])
+    assert bool((whole[:32] == 7.0).all()) and bool((whole[32 + rows:] == 7.0).all())
+
+
+def test_a_row_does_not_depend_on_its_batch():
+    """The sum is exact, so a token's row is the same bytes alone, in a batch, and in an expert's rows."""
+    g = _gen(11)
+    a, sa, b, sb = _operands(g, 700, 512, 1024)
+    want = mxq.int8_scaled_gemm(a, sa, b, sb)
+    for m in (1, 16, 17, 64, 65, 300):
+        assert torch.equal(mxq.int8_scaled_gemm(a[:m], sa[:m], b, sb), want[:m])
+    off = torch.tensor([0, 200, 700], device=DEV)
+    assert torch.equal(mxq.int8_grouped_gemm(a, sa, off, torch.stack([b, b]), torch.stack([sb, sb])), want)
+
+
+def test_products_past_32_bit_offsets():
+    """An output and a weight of more than 2^31 elements and bytes."""
+    g = _gen(3)
+    N, K = 70_000, 32768                                                  # 2.3e9 bytes of weight
+    b = torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    sb = torch.rand(N, generator=g, device=DEV)
+    for M in (2, 80):
+        a, sa = torch.randint(-128, 128, (M, K), generator=g, device=DEV, dtype=torch.int8), torch.rand(M, generator=g, device=DEV)
+        c = mxq.int8_scaled_gemm(a, sa, b, sb)
+        for lo in (0, 40_000, N - 300):
+            _check(c[:, lo:lo + 300], _sums(a, b[lo:lo + 300]), sa, sb[lo:lo + 300], False)
+    del b
+    M, N, K = 40_000, 60_000, 32                                          # 2.4e9 outputs
+    a, sa, b, sb = _operands(g, M, N, K)
+    c = mxq.int8_scaled_gemm(a, sa, b, sb)
+    for lo in (0, 36_000, M - 200):
+        _check(c[lo:lo + 200], _sums(a[lo:lo + 200], b), sa[lo:lo + 200], sb, False)
