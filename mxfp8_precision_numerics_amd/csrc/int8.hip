@@ -150,6 +150,15 @@ struct Int8Gemm {
 // One output from its integer sum. The product is scaled by the token first: sa sb alone could leave fp32's range.
 __device__ __forceinline__ float int8_value(int acc, float sa, float sb) { return ((float)acc * sa) * sb; }
 
+// silu(g) u. The exponential and the quotient are the hardware's (v_exp_f32 and v_rcp_f32, an ulp each), 8 operations of
+// which two take four times as long; the fixed sequence of the MXFP8 path with its division takes about 60, which would cost
+// a 256 x 128 tile more than its matrix instructions at K = 2048. Relative error below (13 + 4.3 |g|) 2^-24, of which
+// 3 (1 + |g|) is g's own; the result is rounded to bf16.
+__device__ __forceinline__ float silu_times(float g, float u) {
+    const float e = __builtin_amdgcn_exp2f(g * -1.44269504f);
+    return (g * __builtin_amdgcn_rcpf(1.0f + e)) * u;
+}
+
 // Rows of B in a tile of TN of them. Plain: TN consecutive rows, TN output columns. SwiGLU: blocks of BLK rows alternate
 // between gate and up rows of the same BLK output columns, so a wave holds both factors of an output in two accumulators.
 template <bool SWIGLU, int BLK>
@@ -254,7 +263,7 @@ __global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Gemm g) {
                 if (n + e >= cols) {
                     v[e] = 0.0f;
                 } else if constexpr (SWIGLU) {
-                    v[e] = swiglu_f32(int8_value(acc[i][j][e], s, sb[n + e]),
+                    v[e] = silu_times(int8_value(acc[i][j][e], s, sb[n + e]),
                                       int8_value(acc[i + 1][j][e], s, sb[cols + n + e]));
                 } else {
                     v[e] = int8_value(acc[i][j][e], s, sb[n + e]);
@@ -272,26 +281,297 @@ __global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Gemm g) {
     }
 }
 
+// ---------------------------------------------------------------------------------------------------------------
+// Large tiles: 256 x 256 rows of A and B per workgroup, one workgroup per CU; 4 waves, 2 x 2, each 128 x 128 as 8 x 8
+// accumulators of 16 x 16 (256 registers). K advances 64 bytes per stage: one v_mfma_i32_16x16x64_i8 per accumulator.
+// (The chip is held back by its power here: from registers alone, on normally distributed codes, this instruction runs
+// at 4.2 POP/s and the 32 x 32 x 32 form at 3.4; on zeros both reach 4.9.) Operand of lane l: row l % 16, bytes 16 (l / 16)
+// .. + 15; B is the first operand, so register e of lane l holds output row l % 16, column 4 (l / 16) + e.
+//
+// LDS holds a ring of five stages (160 KiB), stage s in slot s % 5, 16 KiB for each operand as rows of 64 bytes whose
+// 16-byte chunk c lies at position c ^ ((row / 4) % 4), so that 8 consecutive rows' fragment reads fall on distinct banks.
+// Copies go straight from global memory to LDS. Trip t multiplies stage t from registers and reads stage t + 1's fragments
+// into a second set. Trips go in pairs (t even), with one barrier at a pair's end: when the pair begins, stages t - 1 and t
+// have been read by every wave, so trip t fills the slot of t - 1 with stage t + 4 and trip t + 1 the slot of t with t + 5;
+// t + 1 and t + 2 have landed and are read; t + 3 is on its way. At the pair's end all but t + 5 must have landed, so a stage
+// has one to three trips to arrive, with half the barriers of a ring that joins one every stage.
+constexpr int LT = 256, LK = 64, LSLOTS = 5, LSLOT = 2 * LT * LK;
+constexpr int LGROUP_M = 4;            // row tiles that an XCD's workgroups walk together
+constexpr int64_t LXCD = 32;           // workgroups of one XCD at a time
+
+// acc += b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the instruction
+// another destination and copies results about in the loop. The operands' loads are waited for by the compiler; nothing
+// else may write an operand or read a sum within 19 wait states (the kernel has 64 instructions between two uses of a
+// sum, and waits of its own around the last stage).
+__device__ __forceinline__ void mfma_in_place(v4i& acc, v4i b, v4i a) {
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
+}
+
+template <bool GROUPED, bool SWIGLU>
+__global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
+    __shared__ __attribute__((aligned(16))) uint8_t lds[LSLOTS * LSLOT];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave & 1, wn = wave >> 1;
+    const int64_t cols = SWIGLU ? g.N / 2 : g.N;
+    constexpr int TC = SWIGLU ? LT / 2 : LT;
+    const int tiles_n = (int)((cols + TC - 1) / TC);
+
+    // ------------------------------------------------------------------ tile
+    int64_t m0, m_end, n0, grp = 0;
+    if constexpr (GROUPED) {
+        // each XCD (every eighth workgroup) takes chunks of LXCD consecutive tiles, which share an expert's weights
+        const int64_t nb = gridDim.x, b = blockIdx.x, round = 8 * LXCD;
+        const int64_t t = b < (nb / round) * round ? (b >> 3) / LXCD * round + (b & 7) * LXCD + (b >> 3) % LXCD : b;
+        n0 = (t % tiles_n) * TC;
+        const RowTile rt = find_row_tile<LT>(g.offsets, g.G, g.M, t / tiles_n);
+        if (rt.grp < 0) return;
+        grp = rt.grp;
+        m0 = rt.lo;
+        m_end = rt.lo + LT < rt.hi ? rt.lo + LT : rt.hi;
+    } else {
+        // each XCD walks a contiguous run of an order in groups of LGROUP_M row tiles
+        const int tiles_m = (int)((g.M + LT - 1) / LT);
+        const int T = tiles_m * tiles_n, T8 = T & ~7, b = blockIdx.x;
+        const int v = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
+        const int per_group = LGROUP_M * tiles_n, first_m = (v / per_group) * LGROUP_M;
+        const int gm = min(LGROUP_M, tiles_m - first_m), r = v % per_group;
+        m0 = (int64_t)(first_m + r % gm) * LT;
+        n0 = (int64_t)(r / gm) * TC;
+        m_end = m0 + LT < g.M ? m0 + LT : g.M;
+    }
+    const int8_t* A = g.a + m0 * g.K;
+    const int8_t* B = g.b + (grp * g.N + n0) * g.K;             // SwiGLU: the gate rows; the up rows are cols rows further
+    const int64_t n_end = n0 + TC < cols ? n0 + TC : cols;
+
+    // ------------------------------------------------------------------ scales of the wave's rows and columns
+    // Read here, ahead of the copies, so that the epilogue begins with them in registers.
+    const int r16 = lane & 15, q16 = lane >> 4;
+    constexpr int NB = SWIGLU ? 4 : 8;                          // 16-column output blocks of a wave
+    const float* sb = g.sb + grp * g.N;
+    float sa[8], s_gate[NB][4], s_up[SWIGLU ? NB : 1][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t m = m0 + wm * 128 + j * 16 + r16;
+        sa[j] = g.sa[m < m_end ? m : m_end - 1];
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int64_t n = n0 + wn * (TC / 2) + 16 * b + 4 * q16 + e, nc = n < cols ? n : cols - 1;
+            s_gate[b][e] = sb[nc];
+            if constexpr (SWIGLU) s_up[b][e] = sb[cols + nc];
+        }
+
+    // ------------------------------------------------------------------ copies
+    // Copy c (0 .. 3) of a wave fills rows 64c + 16 wave .. + 15 of a slot's operand: lane l brings chunk
+    // (l % 4) ^ (row / 4 % 4) of row l / 4 among them. Rows past an operand's end are clamped to its last row (their outputs
+    // are never stored); the resources end with the operand, so the last half of a stage past K reads zeros at its very end.
+    auto bytes = [&](int64_t rows) { return (uint32_t)(rows * g.K < 0x7FFFFFFF ? rows * g.K : 0x7FFFFFFF); };
+    const v4i rA = buffer_rsrc(A, bytes(g.M - m0));
+    const v4i rB = buffer_rsrc(B, bytes(cols - n0));
+    const v4i rU = SWIGLU ? buffer_rsrc(B + cols * g.K, bytes(cols - n0)) : rB;
+    int a_off[4], b_off[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int row = 64 * c + 16 * wave + (lane >> 2), chunk = (lane & 3) ^ ((lane >> 4) & 3);
+        const int col = SWIGLU ? 16 * (row / 32) + row % 16 : row;            // the output column of B's row
+        const int ar = m0 + row < m_end ? row : (int)(m_end - 1 - m0);
+        const int br = n0 + col < n_end ? col : (int)(n_end - 1 - n0);
+        a_off[c] = ar * (int)g.K + 16 * chunk;
+        b_off[c] = br * (int)g.K + 16 * chunk;
+    }
+    const bool up = SWIGLU && (wave & 1);                       // rows 16 .. 31 of every 32 are up rows
+    const v4i rBw = up ? rU : rB;
+    const uint32_t lds0 = lds_offset(&lds[1024 * wave]);
+    // copy c (0 .. 7: A, then B) of stage s into slot at byte `slot`
+    auto copy = [&](int s, uint32_t slot, int c) {
+        if (c < 4) dma_to_lds<16>(rA, lds0 + slot + 4096 * c, a_off[c], s * LK);
+        else dma_to_lds<16>(rBw, lds0 + slot + LT * LK + 4096 * (c - 4), b_off[c - 4], s * LK);
+    };
+    auto next_slot = [](uint32_t slot) { return slot == (LSLOTS - 1) * LSLOT ? 0u : slot + LSLOT; };
+
+    // ------------------------------------------------------------------ fragments and matrix instructions
+    const int in_row = r16 * LK + 16 * (q16 ^ ((r16 >> 2) & 3));
+    const int at_a = wm * 128 * LK + in_row, at_b = LT * LK + wn * 128 * LK + in_row;
+    // fragment f of a stage (0 .. 7: A rows 16f .., 8 .. 15: B rows 16 (f - 8) .. of the wave)
+    auto frag = [&](uint32_t slot, int f) {
+        return *reinterpret_cast<const v4i*>(&lds[slot + (f < 8 ? at_a + f * 16 * LK : at_b + (f - 8) * 16 * LK)]);
+    };
+    v4i acc[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    v4i F[2][16];                                               // two sets of fragments
+
+    // One trip in 16 steps of 4 instructions: the stage in set P is multiplied; with READ, the next stage's fragments are
+    // read from `slot` into the other set, two in each of the first 8 steps; with COPY, the 8 copies of stage s go to
+    // `into`, one in every other step.
+    auto trip = [&](auto p_c, auto read_c, uint32_t slot, auto copy_c, int s, uint32_t into) {
+        constexpr int P = decltype(p_c)::value;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+            const int i = q >> 1;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int j = 4 * (q & 1) + x;
+                mfma_in_place(acc[i][j], F[P][8 + i], F[P][j]);
+            }
+            if constexpr (decltype(read_c)::value) {
+                if (q < 8) {
+                    F[P ^ 1][2 * q] = frag(slot, 2 * q);
+                    F[P ^ 1][2 * q + 1] = frag(slot, 2 * q + 1);
+                }
+            }
+            if constexpr (decltype(copy_c)::value) {
+                if (q & 1) copy(s, into, q >> 1);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    using T0 = std::integral_constant<int, 0>;
+    using T1 = std::integral_constant<int, 1>;
+    constexpr std::true_type yes{};
+    constexpr std::false_type no{};
+
+    // ------------------------------------------------------------------ prologue: stages 0 .. 3
+    const int nk = (int)((g.K + LK - 1) / LK);
+    const bool half_last = g.K % LK != 0;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        if (s < nk) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) copy(s, s * LSLOT, c);
+        }
+    }
+    if (nk > 3) wait_copies_barrier<8>();
+    else wait_copies_barrier<0>();
+#pragma unroll
+    for (int f = 0; f < 16; ++f) F[0][f] = frag(0, f);
+    wait_copies_barrier<8>();                                   // every wave has read stage 0
+    __builtin_amdgcn_s_waitcnt(0xC07F);                         // the compiler's own view of that wait
+
+    // ------------------------------------------------------------------ pairs of trips
+    int t = 0;
+    uint32_t s0 = 0;                                            // slot of stage t
+    for (; t + 5 < nk; t += 2) {
+        const uint32_t s1 = next_slot(s0), s2 = next_slot(s1), last = s0 == 0 ? (LSLOTS - 1) * LSLOT : s0 - LSLOT;
+        trip(T0{}, yes, s1, yes, t + 4, last);
+        trip(T1{}, yes, s2, yes, t + 5, s0);
+        wait_copies_barrier<8>();
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        s0 = s2;
+    }
+    // the last pairs: at most stage t + 4 is still to be copied
+    for (; t + 2 < nk; t += 2) {
+        const uint32_t s1 = next_slot(s0), s2 = next_slot(s1), last = s0 == 0 ? (LSLOTS - 1) * LSLOT : s0 - LSLOT;
+        if (t + 4 < nk) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) copy(t + 4, last, c);
+        }
+        trip(T0{}, yes, s1, no, 0, 0);
+        trip(T1{}, yes, s2, no, 0, 0);
+        wait_copies_barrier<0>();
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        s0 = s2;
+    }
+    if (t + 1 < nk) {
+        trip(T0{}, yes, next_slot(s0), no, 0, 0);
+#pragma unroll
+        for (int f = 0; f < 16; ++f) F[0][f] = F[1][f];
+    }
+    // the last stage; where it holds 32 bytes, the second half of A's rows becomes zeros (a select: the accumulators keep
+    // one path)
+    const int keep = half_last && q16 >= 2 ? 0 : -1;
+#pragma unroll
+    for (int f = 0; f < 8; ++f)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) F[0][f][e] &= keep;
+    asm volatile("s_nop 7");                                    // the selects' results to the matrix instructions
+    trip(T0{}, no, 0, no, 0, 0);
+    asm volatile("s_nop 15\n\ts_nop 15");                       // the matrix instructions' results to what reads them
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm volatile("" : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]),
+                          "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
+
+    // ------------------------------------------------------------------ epilogue
+    // Lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block. Two blocks side by side swap every other
+    // 16-lane row (v_permlane16_swap), which leaves a lane with 8 consecutive columns of one of them: lanes of row R hold
+    // columns 16 (R % 2) + 8 (R / 2) .. of the pair's 32, and a 16-byte store writes 64 contiguous bytes into each of 16
+    // rows.
+    const bool vec_ok = (g.ldc & 7) == 0 && (reinterpret_cast<uintptr_t>(g.c) & 15) == 0;
+#pragma unroll
+    for (int p = 0; p < NB / 2; ++p) {
+        const int64_t n = n0 + wn * (TC / 2) + p * 32 + 16 * (q16 & 1) + 8 * (q16 >> 1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int b = 2 * p + h;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (SWIGLU)
+                        v[e] = silu_times(int8_value(acc[2 * b][j][e], sa[j], s_gate[b][e]),
+                                          int8_value(acc[2 * b + 1][j][e], sa[j], s_up[b][e]));
+                    else
+                        v[e] = int8_value(acc[b][j][e], sa[j], s_gate[b][e]);
+                }
+                w[h][0] = pack_bf16(v[0], v[1]);
+                w[h][1] = pack_bf16(v[2], v[3]);
+            }
+            const auto x = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
+            const auto y = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
+            const int64_t m = m0 + wm * 128 + j * 16 + r16;
+            if (m >= m_end) continue;
+            uint16_t* dst = g.c + m * g.ldc + n;
+            const uint32_t d[4] = {(uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]};
+            if (vec_ok && n + 8 <= n_end) {
+                *reinterpret_cast<uint4*>(dst) = make_uint4(d[0], d[1], d[2], d[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (n + e < n_end) dst[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+    }
+}
+
 // Upper bound of the row tiles of TH rows over ragged groups: every group with rows adds at most one partial tile.
 static int64_t most_row_tiles(int64_t rows, int64_t G, int64_t TH) { return (rows + TH - 1) / TH + (G < rows ? G : rows); }
 
+// Large tiles where they fill the chip: at least 512 rows and output columns (grouped: 512 rows an expert on average).
+static bool large_tiles(int64_t M, int64_t cols, int64_t G) { return cols >= 512 && M >= 512 * (G ? G : 1); }
+
 int64_t int8_gemm_blocks(int64_t M, int64_t cols, int64_t G, int swiglu) {
-    const int64_t tc = swiglu ? QT / 2 : QT;
-    const int64_t tiles_n = (cols + tc - 1) / tc, tiles_m = G ? most_row_tiles(M, G, QT) : (M + QT - 1) / QT;
+    const int64_t tile = large_tiles(M, cols, G) ? LT : QT, tc = swiglu ? tile / 2 : tile;
+    const int64_t tiles_n = (cols + tc - 1) / tc, tiles_m = G ? most_row_tiles(M, G, tile) : (M + tile - 1) / tile;
     return tiles_n > 0 && tiles_m > INT64_MAX / tiles_n ? INT64_MAX : tiles_m * tiles_n;
+}
+
+template <bool GROUPED, bool SWIGLU>
+static void launch_products(const Int8Gemm& g, int64_t cols, hipStream_t stream) {
+    const dim3 blocks((unsigned)int8_gemm_blocks(g.M, cols, g.G, SWIGLU));
+    if (large_tiles(g.M, cols, g.G))
+        hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU>), blocks, dim3(256), 0, stream, g);
+    else
+        hipLaunchKernelGGL((int8_gemm_kernel<GROUPED, SWIGLU>), blocks, dim3(256), 0, stream, g);
 }
 
 hipError_t launch_int8_gemm(const int8_t* a_q, const float* a_scale, const int64_t* offsets, int64_t G, int64_t M,
                             const int8_t* b_q, const float* b_scale, int64_t N, int64_t K, int swiglu, uint16_t* c,
                             int64_t ldc, hipStream_t stream) {
     const Int8Gemm g{a_q, b_q, a_scale, b_scale, c, M, N, K, ldc, offsets, G};
-    const dim3 blocks((unsigned)int8_gemm_blocks(M, swiglu ? N / 2 : N, G, swiglu));
     if (G) {
-        if (swiglu) hipLaunchKernelGGL((int8_gemm_kernel<true, true>), blocks, dim3(256), 0, stream, g);
-        else hipLaunchKernelGGL((int8_gemm_kernel<true, false>), blocks, dim3(256), 0, stream, g);
+        if (swiglu) launch_products<true, true>(g, N / 2, stream);
+        else launch_products<true, false>(g, N, stream);
     } else {
-        if (swiglu) hipLaunchKernelGGL((int8_gemm_kernel<false, true>), blocks, dim3(256), 0, stream, g);
-        else hipLaunchKernelGGL((int8_gemm_kernel<false, false>), blocks, dim3(256), 0, stream, g);
+        if (swiglu) launch_products<false, true>(g, N / 2, stream);
+        else launch_products<false, false>(g, N, stream);
     }
     return hipGetLastError();
 }
