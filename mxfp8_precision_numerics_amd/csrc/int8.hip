@@ -288,14 +288,15 @@ __global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Gemm g) {
 // at 4.2 POP/s and the 32 x 32 x 32 form at 3.4; on zeros both reach 4.9.) Operand of lane l: row l % 16, bytes 16 (l / 16)
 // .. + 15; B is the first operand, so register e of lane l holds output row l % 16, column 4 (l / 16) + e.
 //
-// LDS holds a ring of five stages (160 KiB), stage s in slot s % 5, 16 KiB for each operand as rows of 64 bytes whose
-// 16-byte chunk c lies at position c ^ ((row / 4) % 4), so that 8 consecutive rows' fragment reads fall on distinct banks.
-// Copies go straight from global memory to LDS. Trip t multiplies stage t from registers and reads stage t + 1's fragments
-// into a second set. Trips go in pairs (t even), with one barrier at a pair's end: when the pair begins, stages t - 1 and t
-// have been read by every wave, so trip t fills the slot of t - 1 with stage t + 4 and trip t + 1 the slot of t with t + 5;
-// t + 1 and t + 2 have landed and are read; t + 3 is on its way. At the pair's end all but t + 5 must have landed, so a stage
-// has one to three trips to arrive, with half the barriers of a ring that joins one every stage.
-constexpr int LT = 256, LK = 64, LSLOTS = 5, LSLOT = 2 * LT * LK;
+// K advances in pairs of stages, 128 bytes, so that a copy instruction (global to LDS, no registers) takes whole lines: 8
+// rows of 128 bytes. (16 rows of 64 bytes a copy, twice the requests to the L2, cost 1.13 times the time at
+// 4096 x 36864 x 12288.) LDS holds three pairs of A and two of B, 32 KiB each, as rows of 128 bytes whose 16-byte chunk c
+// lies at position c ^ (row / 2 % 8): the fragment reads of 16 consecutive rows fall on all banks once.
+// Trip t multiplies stage t from registers and reads stage t + 1's fragments into a second set; the one barrier of a pair
+// lies behind its first trip, where every wave has read the whole pair p: trip 2p + 1 then copies B's pair p + 2 into B's
+// region of p, trip 2p + 2 A's pair p + 3 into A's region of p. At the next barrier, behind trip 2p + 2, all but that last
+// pair of A must have landed: B has one to two trips to arrive, A three to four.
+constexpr int LT = 256, LK = 64, LPAIR = 2 * LK, LREGION = LT * LPAIR, LREGIONS_A = 3;
 constexpr int LGROUP_M = 4;            // row tiles that an XCD's workgroups walk together
 constexpr int64_t LXCD = 32;           // workgroups of one XCD at a time
 
@@ -309,7 +310,7 @@ __device__ __forceinline__ void mfma_in_place(v4i& acc, v4i b, v4i a) {
 
 template <bool GROUPED, bool SWIGLU>
 __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[LSLOTS * LSLOT];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[(LREGIONS_A + 2) * LREGION];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
@@ -365,51 +366,47 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
         }
 
     // ------------------------------------------------------------------ copies
-    // Copy c (0 .. 3) of a wave fills rows 64c + 16 wave .. + 15 of a slot's operand: lane l brings chunk
-    // (l % 4) ^ (row / 4 % 4) of row l / 4 among them. Rows past an operand's end are clamped to its last row (their outputs
-    // are never stored); the resources end with the operand, so the last half of a stage past K reads zeros at its very end.
+    // Copy c (0 .. 7) of a wave fills rows 32c + 8 wave .. + 7 of a region: lane l brings row l / 8 of them, the chunk that
+    // belongs at position l % 8. The resources end with the operand: rows behind its end are zeros, rows of A behind the
+    // group's are the next group's, and what a last pair asks for past the end of K is a part of the next row (their
+    // outputs are never stored, and the last is masked).
     auto bytes = [&](int64_t rows) { return (uint32_t)(rows * g.K < 0x7FFFFFFF ? rows * g.K : 0x7FFFFFFF); };
     const v4i rA = buffer_rsrc(A, bytes(g.M - m0));
-    const v4i rB = buffer_rsrc(B, bytes(cols - n0));
-    const v4i rU = SWIGLU ? buffer_rsrc(B + cols * g.K, bytes(cols - n0)) : rB;
-    int a_off[4], b_off[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int row = 64 * c + 16 * wave + (lane >> 2), chunk = (lane & 3) ^ ((lane >> 4) & 3);
-        const int col = SWIGLU ? 16 * (row / 32) + row % 16 : row;            // the output column of B's row
-        const int ar = m0 + row < m_end ? row : (int)(m_end - 1 - m0);
-        const int br = n0 + col < n_end ? col : (int)(n_end - 1 - n0);
-        a_off[c] = ar * (int)g.K + 16 * chunk;
-        b_off[c] = br * (int)g.K + 16 * chunk;
-    }
-    const bool up = SWIGLU && (wave & 1);                       // rows 16 .. 31 of every 32 are up rows
-    const v4i rBw = up ? rU : rB;
+    const v4i rB = buffer_rsrc(SWIGLU && wave >= 2 ? B + cols * g.K : B, bytes(cols - n0));   // waves 2, 3 bring up rows
+    const int brow = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
+    const int K = (int)g.K;
+    const int a_off = brow * K + 16 * chunk, b_off = (SWIGLU ? brow & 15 : brow) * K + 16 * chunk;
+    const int a_step = 32 * K, b_step = SWIGLU ? 16 * K : 32 * K;
     const uint32_t lds0 = lds_offset(&lds[1024 * wave]);
-    // copy c (0 .. 7: A, then B) of stage s into slot at byte `slot`
-    auto copy = [&](int s, uint32_t slot, int c) {
-        if (c < 4) dma_to_lds<16>(rA, lds0 + slot + 4096 * c, a_off[c], s * LK);
-        else dma_to_lds<16>(rBw, lds0 + slot + LT * LK + 4096 * (c - 4), b_off[c - 4], s * LK);
-    };
-    auto next_slot = [](uint32_t slot) { return slot == (LSLOTS - 1) * LSLOT ? 0u : slot + LSLOT; };
+    // copy c of pair p into the region at byte `into`
+    auto copy_a = [&](int p, uint32_t into, int c) { dma_to_lds<16>(rA, lds0 + into + 4096 * c, a_off + c * a_step, p * LPAIR); };
+    auto copy_b = [&](int p, uint32_t into, int c) { dma_to_lds<16>(rB, lds0 + into + 4096 * c, b_off + c * b_step, p * LPAIR); };
+    constexpr uint32_t B0 = LREGIONS_A * LREGION;               // B's regions
 
     // ------------------------------------------------------------------ fragments and matrix instructions
-    const int in_row = r16 * LK + 16 * (q16 ^ ((r16 >> 2) & 3));
-    const int at_a = wm * 128 * LK + in_row, at_b = LT * LK + wn * 128 * LK + in_row;
-    // fragment f of a stage (0 .. 7: A rows 16f .., 8 .. 15: B rows 16 (f - 8) .. of the wave)
-    auto frag = [&](uint32_t slot, int f) {
-        return *reinterpret_cast<const v4i*>(&lds[slot + (f < 8 ? at_a + f * 16 * LK : at_b + (f - 8) * 16 * LK)]);
+    const int in_row[2] = {r16 * LPAIR + 16 * (q16 ^ (r16 >> 1)), r16 * LPAIR + 16 * ((4 + q16) ^ (r16 >> 1))};
+    // fragment f (0 .. 7: A rows 16f .., 8 .. 15: B rows 16 (f - 8) .. of the wave) of half h of the pair in regions a and b
+    auto frag = [&](uint32_t a, uint32_t b, int h, int f) {
+        const uint32_t at = f < 8 ? a + wm * 128 * LPAIR + f * 16 * LPAIR : b + wn * 128 * LPAIR + (f - 8) * 16 * LPAIR;
+        return *reinterpret_cast<const v4i*>(&lds[at + in_row[h]]);
     };
     v4i acc[8][8];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    // Everything that writes the sums before this statement has been issued, and nothing that reads them has.
+    auto settle = [&]() {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            asm volatile("" : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]),
+                              "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
+    };
     v4i F[2][16];                                               // two sets of fragments
 
-    // One trip in 16 steps of 4 instructions: the stage in set P is multiplied; with READ, the next stage's fragments are
-    // read from `slot` into the other set, two in each of the first 8 steps; with COPY, the 8 copies of stage s go to
-    // `into`, one in every other step.
-    auto trip = [&](auto p_c, auto read_c, uint32_t slot, auto copy_c, int s, uint32_t into) {
+    // One trip in 16 steps of 4 instructions: set P is multiplied; with READ, half P ^ 1 of the pair in regions (a, b) is read
+    // into the other set, two fragments in each of the first 8 steps; a copy (copy(c), c = 0 .. 7) goes in every other step.
+    auto trip = [&](auto p_c, auto read_c, uint32_t a, uint32_t b, auto&& copy) {
         constexpr int P = decltype(p_c)::value;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -421,13 +418,11 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
             }
             if constexpr (decltype(read_c)::value) {
                 if (q < 8) {
-                    F[P ^ 1][2 * q] = frag(slot, 2 * q);
-                    F[P ^ 1][2 * q + 1] = frag(slot, 2 * q + 1);
+                    F[P ^ 1][2 * q] = frag(a, b, P ^ 1, 2 * q);
+                    F[P ^ 1][2 * q + 1] = frag(a, b, P ^ 1, 2 * q + 1);
                 }
             }
-            if constexpr (decltype(copy_c)::value) {
-                if (q & 1) copy(s, into, q >> 1);
-            }
+            if (q & 1) copy(q >> 1);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -435,67 +430,85 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     using T1 = std::integral_constant<int, 1>;
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
+    auto none = [](int) {};
+    // What a last pair holds past K becomes zero in A (selects: the sums keep one path).
+    const int rem = (int)(g.K % LPAIR);                         // 0, 32, 64 or 96
+    auto mask = [&](auto p_c) {
+        constexpr int P = decltype(p_c)::value;
+        const int keep = rem == 0 || 16 * (4 * P + q16) < rem ? -1 : 0;
+#pragma unroll
+        for (int f = 0; f < 8; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) F[P][f][e] &= keep;
+        // the selects' results to the matrix instructions
+        asm volatile("s_nop 7" : "+v"(F[P][0]), "+v"(F[P][1]), "+v"(F[P][2]), "+v"(F[P][3]), "+v"(F[P][4]), "+v"(F[P][5]),
+                                 "+v"(F[P][6]), "+v"(F[P][7]));
+    };
 
-    // ------------------------------------------------------------------ prologue: stages 0 .. 3
-    const int nk = (int)((g.K + LK - 1) / LK);
-    const bool half_last = g.K % LK != 0;
+    // ------------------------------------------------------------------ prologue: pairs 0 and 1, and A's pair 2
+    const int np = (int)((g.K + LPAIR - 1) / LPAIR);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        if (s < nk) {
+    for (int c = 0; c < 8; ++c) copy_a(0, 0, c);
 #pragma unroll
-            for (int c = 0; c < 8; ++c) copy(s, s * LSLOT, c);
-        }
+    for (int c = 0; c < 8; ++c) copy_b(0, B0, c);
+    if (np > 1) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) copy_a(1, LREGION, c);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) copy_b(1, B0 + LREGION, c);
     }
-    if (nk > 3) wait_copies_barrier<8>();
+    if (np > 2) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) copy_a(2, 2 * LREGION, c);
+    }
+    settle();                                                   // the zeros are written while the first pairs are on their way
+    if (np > 2) wait_copies_barrier<24>();
+    else if (np > 1) wait_copies_barrier<16>();
     else wait_copies_barrier<0>();
 #pragma unroll
-    for (int f = 0; f < 16; ++f) F[0][f] = frag(0, f);
-    wait_copies_barrier<8>();                                   // every wave has read stage 0
+    for (int f = 0; f < 16; ++f) F[0][f] = frag(0, B0, 0, f);
+    if (np == 1) mask(T0{});
+    trip(T0{}, yes, 0, B0, none);
+    if (np > 2) wait_copies_barrier<8>();
+    else wait_copies_barrier<0>();
     __builtin_amdgcn_s_waitcnt(0xC07F);                         // the compiler's own view of that wait
 
-    // ------------------------------------------------------------------ pairs of trips
-    int t = 0;
-    uint32_t s0 = 0;                                            // slot of stage t
-    for (; t + 5 < nk; t += 2) {
-        const uint32_t s1 = next_slot(s0), s2 = next_slot(s1), last = s0 == 0 ? (LSLOTS - 1) * LSLOT : s0 - LSLOT;
-        trip(T0{}, yes, s1, yes, t + 4, last);
-        trip(T1{}, yes, s2, yes, t + 5, s0);
+    // ------------------------------------------------------------------ pairs
+    int p = 0;
+    uint32_t a0 = 0, a1 = LREGION, b0 = B0, b1 = B0 + LREGION;  // regions of pairs p and p + 1
+    auto next = [&]() {
+        a0 = a1;
+        a1 = a1 == 2 * LREGION ? 0u : a1 + LREGION;
+        const uint32_t x = b0;
+        b0 = b1;
+        b1 = x;
+        ++p;
+    };
+    while (p + 3 < np) {
+        trip(T1{}, yes, a1, b1, [&](int c) { copy_b(p + 2, b0, c); });
+        trip(T0{}, yes, a1, b1, [&](int c) { copy_a(p + 3, a0, c); });
         wait_copies_barrier<8>();
         __builtin_amdgcn_s_waitcnt(0xC07F);
-        s0 = s2;
+        next();
     }
-    // the last pairs: at most stage t + 4 is still to be copied
-    for (; t + 2 < nk; t += 2) {
-        const uint32_t s1 = next_slot(s0), s2 = next_slot(s1), last = s0 == 0 ? (LSLOTS - 1) * LSLOT : s0 - LSLOT;
-        if (t + 4 < nk) {
+    while (p + 1 < np) {                                        // at most B's pair p + 2 is still to be copied
+        if (p + 2 < np) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) copy(t + 4, last, c);
+            for (int c = 0; c < 8; ++c) copy_b(p + 2, b0, c);
         }
-        trip(T0{}, yes, s1, no, 0, 0);
-        trip(T1{}, yes, s2, no, 0, 0);
+        trip(T1{}, yes, a1, b1, none);
+        if (p + 2 == np && rem) mask(T0{});
+        trip(T0{}, yes, a1, b1, none);
         wait_copies_barrier<0>();
         __builtin_amdgcn_s_waitcnt(0xC07F);
-        s0 = s2;
+        next();
     }
-    if (t + 1 < nk) {
-        trip(T0{}, yes, next_slot(s0), no, 0, 0);
-#pragma unroll
-        for (int f = 0; f < 16; ++f) F[0][f] = F[1][f];
+    if (rem == 0 || rem > LK) {                                 // the last half, if K reaches into it
+        if (rem) mask(T1{});
+        trip(T1{}, no, 0, 0, none);
     }
-    // the last stage; where it holds 32 bytes, the second half of A's rows becomes zeros (a select: the accumulators keep
-    // one path)
-    const int keep = half_last && q16 >= 2 ? 0 : -1;
-#pragma unroll
-    for (int f = 0; f < 8; ++f)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) F[0][f][e] &= keep;
-    asm volatile("s_nop 7");                                    // the selects' results to the matrix instructions
-    trip(T0{}, no, 0, no, 0, 0);
     asm volatile("s_nop 15\n\ts_nop 15");                       // the matrix instructions' results to what reads them
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        asm volatile("" : "+a"(acc[i][0]), "+a"(acc[i][1]), "+a"(acc[i][2]), "+a"(acc[i][3]), "+a"(acc[i][4]),
-                          "+a"(acc[i][5]), "+a"(acc[i][6]), "+a"(acc[i][7]));
+    settle();
 
     // ------------------------------------------------------------------ epilogue
     // Lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block. Two blocks side by side swap every other

@@ -1,0 +1,81 @@
+"""The int8 products issue their matrix instructions as assembly, whose results the compiler does not know to wait for. This
+reads the code built from csrc/int8.hip: around every such instruction nothing may read or write its sum too early, no
+operand may have been written just before it, and no sum may live in scratch memory."""
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+
+OBJ = os.path.join(ROOT, "mxfp8_precision_numerics_amd", "_build", "int8.o")
+LLVM = "/opt/rocm/llvm/bin"
+AFTER = 18        # wait states from a matrix instruction's issue to another kind's use of its result (16 x 16: at most 8 passes)
+BEFORE = 2        # from a vector instruction's write to a matrix instruction's read
+
+
+def _kernels(tmp):
+    for tool in ("llvm-objcopy", "clang-offload-bundler", "llvm-objdump"):
+        if not os.path.exists(os.path.join(LLVM, tool)):
+            pytest.skip(f"no {tool}")
+    if not os.path.exists(OBJ):
+        pytest.skip("the build's intermediate files are not here")
+    run = lambda *a: subprocess.run(a, check=True, capture_output=True, text=True).stdout  # noqa: E731
+    obj, fat, co = (os.path.join(tmp, n) for n in ("int8.o", "fat", "co"))
+    shutil.copy(OBJ, obj)
+    run(f"{LLVM}/llvm-objcopy", f"--dump-section=.hip_fatbin={fat}", obj)
+    target = [t for t in run(f"{LLVM}/clang-offload-bundler", "--list", "--type=o", f"--input={fat}").split() if "gfx950" in t][0]
+    run(f"{LLVM}/clang-offload-bundler", "--unbundle", "--type=o", f"--targets={target}", f"--input={fat}", f"--output={co}")
+    name, code = None, {}
+    for line in run(f"{LLVM}/llvm-objdump", "-d", "--no-show-raw-insn", co).splitlines():
+        m = re.match(r"^[0-9a-f]+ <(\w+)>:", line)
+        if m:
+            name = m.group(1)
+            code[name] = []
+        elif name and line.startswith("\t"):
+            code[name].append(line.split("//")[0].strip())
+    return code
+
+
+def _registers(operand):
+    """The vector registers an operand names: {('v', n), ('a', n), ...}."""
+    found = set()
+    for kind, one, lo, hi in re.findall(r"\b([va])(?:(\d+)|\[(\d+):(\d+)\])", operand):
+        lo, hi = (int(one), int(one)) if one else (int(lo), int(hi))
+        found |= {(kind, n) for n in range(lo, hi + 1)}
+    return found
+
+
+def _states(insn):
+    m = re.match(r"s_nop (\w+)", insn)
+    return int(m.group(1), 0) + 1 if m else 1
+
+
+def test_large_tile_kernels(tmp_path):
+    code = {n: c for n, c in _kernels(str(tmp_path)).items() if "int8_gemm_large_kernel" in n}
+    assert len(code) == 4
+    for name, insns in code.items():
+        assert not any(i.startswith("scratch_") for i in insns), name
+        issued, written = {}, {}                     # register -> wait states since, in the order of the code
+        now, count = 0, 0
+        for insn in insns:
+            op, _, rest = insn.partition(" ")
+            operands = [o.strip() for o in re.split(r",(?![^\[]*\])", rest)] if rest else []
+            if op.startswith("v_mfma"):
+                count += 1
+                dst = _registers(operands[0])
+                assert operands[0] == operands[3], (name, insn)          # in place
+                for r in _registers(operands[1]) | _registers(operands[2]) | dst:
+                    assert now - written.get(r, -99) > BEFORE, (name, insn)
+                for r in dst:
+                    issued[r] = now
+            elif op.startswith(("v_", "ds_", "global_", "buffer_", "flat_")):
+                for r in _registers(rest):
+                    assert now - issued.get(r, -99) > AFTER, (name, insn)
+                if op.startswith("v_") and operands:
+                    for r in _registers(operands[0]):
+                        written[r] = now
+            now += _states(insn)
+        assert count > 300, name
