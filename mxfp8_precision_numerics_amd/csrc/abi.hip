@@ -68,7 +68,7 @@ mxq_status int8_gemm_shape(int64_t M, int64_t N, int64_t K, int64_t G, int swigl
     const int64_t cols = swiglu ? N / 2 : N;
     if (ldc < cols) return MXQ_ERR_SHAPE;
     if (M > (int64_t(1) << 40) || N > (int64_t(1) << 30) || ldc > (int64_t(1) << 40)) return MXQ_ERR_SHAPE;
-    if (M && cols && mxq::int8_gemm_blocks(M, cols, G, swiglu) > mxq::kMaxThreads / 256) return MXQ_ERR_SHAPE;
+    if (M && cols && !mxq::int8_gemm_fits(M, cols, K, G, swiglu)) return MXQ_ERR_SHAPE;
     return MXQ_OK;
 }
 

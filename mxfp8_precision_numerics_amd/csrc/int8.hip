@@ -159,115 +159,299 @@ __device__ __forceinline__ float silu_times(float g, float u) {
     return (g * __builtin_amdgcn_rcpf(1.0f + e)) * u;
 }
 
-// Rows of B in a tile of TN of them. Plain: TN consecutive rows, TN output columns. SwiGLU: blocks of BLK rows alternate
-// between gate and up rows of the same BLK output columns, so a wave holds both factors of an output in two accumulators.
-template <bool SWIGLU, int BLK>
-__device__ __forceinline__ int64_t b_row(int64_t n0, int r, int64_t F) {
-    if constexpr (!SWIGLU) return n0 + r;
-    else return n0 + (r / (2 * BLK)) * BLK + r % BLK + ((r / BLK) & 1) * F;
+// Rows of B in a tile with SwiGLU: blocks of 16 alternate between gate rows and the up rows of the same 16 output columns, so a
+// wave holds both factors of an output in two accumulators.
+
+// The tile of a workgroup: TM rows of A within one group, and the index of its column tile.
+struct Int8Tile {
+    int64_t m0, m_end, grp, n;      // grp < 0: none
+};
+constexpr int GROUP_M = 4;              // row tiles that an XCD's workgroups walk together
+constexpr int64_t XCD_CHUNK = 32;       // consecutive tiles that an XCD takes at a time (grouped)
+
+template <int TM, bool GROUPED>
+__device__ __forceinline__ Int8Tile tile_of(const Int8Gemm& g, int tiles_n) {
+    Int8Tile r;
+    r.grp = 0;
+    if constexpr (GROUPED) {
+        // each XCD (every eighth workgroup) takes chunks of consecutive tiles, which share an expert's weights
+        const int64_t nb = gridDim.x, b = blockIdx.x, round = 8 * XCD_CHUNK;
+        const int64_t t = b < (nb / round) * round ? (b >> 3) / XCD_CHUNK * round + (b & 7) * XCD_CHUNK + (b >> 3) % XCD_CHUNK : b;
+        r.n = t % tiles_n;
+        const RowTile rt = find_row_tile<TM>(g.offsets, g.G, g.M, t / tiles_n);
+        r.grp = rt.grp;
+        r.m0 = rt.lo;
+        r.m_end = rt.lo + TM < rt.hi ? rt.lo + TM : rt.hi;
+    } else {
+        // each XCD walks a contiguous run of an order in groups of GROUP_M row tiles
+        const int tiles_m = (int)((g.M + TM - 1) / TM);
+        const int T = tiles_m * tiles_n, T8 = T & ~7, b = blockIdx.x;
+        const int v = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
+        const int per_group = GROUP_M * tiles_n, first_m = (v / per_group) * GROUP_M;
+        const int gm = min(GROUP_M, tiles_m - first_m), x = v % per_group;
+        r.m0 = (int64_t)(first_m + x % gm) * TM;
+        r.n = x / gm;
+        r.m_end = r.m0 + TM < g.M ? r.m0 + TM : g.M;
+    }
+    return r;
 }
 
-// 128 x 128 rows of A and B per workgroup (4 waves, 2 x 2, each 64 x 64 as 4 x 4 v_mfma_i32_16x16x64_i8). K advances 128
-// bytes per stage, staged through registers into two LDS buffers of 128-byte rows whose 16-byte chunks are XOR-swizzled by
-// the row. B is the instruction's first operand: lane l, register e hold output row l % 16, column 4 (l / 16) + e.
-constexpr int QT = 128, QK = 128;
-__device__ __forceinline__ int q_swz(int row, int chunk) { return row * QK + ((chunk ^ (row & 7)) << 4); }
+// Where in its contraction a workgroup begins (of n steps, then around): spread evenly over consecutive tiles. Workgroups that
+// walk rows of the same length in step would ask the same few memory channels at any time; the order of an exact sum is free.
+__device__ __forceinline__ int first_step(uint32_t tile, int n) {
+    return __builtin_amdgcn_readfirstlane((int)(((uint64_t)(tile * 0x9E3779B9u) * (uint32_t)n) >> 32));
+}
 
-template <bool GROUPED, bool SWIGLU>
+// Resource of an operand's rows from `p` on, `rows` of them to the operand's end: what lies behind reads as zeros.
+__device__ __forceinline__ v4i rows_rsrc(const int8_t* p, int64_t rows, int64_t K) {
+    return buffer_rsrc(p, (uint32_t)(rows * K < 0x7FFFFFFF ? rows * K : 0x7FFFFFFF));
+}
+
+// Middle tiles: 64 rows of A by 128 rows of B per workgroup; 4 waves side by side, each 64 x 32, as 16 x 16 accumulators of
+// v_mfma_i32_16x16x64_i8. K advances 128 bytes per stage; a ring of DEPTH stages in LDS, filled by copies of whole lines, rows
+// of 128 bytes whose 16-byte chunk c lies at position c ^ (row / 2 % 8). One barrier a stage: behind it the stage has landed for
+// every wave and the one before it has been read, so its place is filled with the stage DEPTH - 1 ahead. B is the instruction's
+// first operand: lane l, register e hold output row l % 16, column 4 (l / 16) + e. (128 x 128 tiles, two to a CU, were within
+// 5% of the better of these and the large ones, or behind, at 130 to 2048 rows.)
+constexpr int MT_M = 64, MT_N = 128;
+template <int DEPTH, bool GROUPED, bool SWIGLU>
 __global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Gemm g) {
-    __shared__ __attribute__((aligned(16))) uint8_t sA[2][QT * QK];
-    __shared__ __attribute__((aligned(16))) uint8_t sB[2][QT * QK];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int wm = wave & 1, wn = wave >> 1;
-    const int64_t cols = SWIGLU ? g.N / 2 : g.N;                 // output columns
-    constexpr int TC = SWIGLU ? QT / 2 : QT;                     // of a tile
-    const int64_t tiles_n = (cols + TC - 1) / TC;
-    int64_t m0, m_end, grp = 0;
-    const int64_t n0 = (blockIdx.x % tiles_n) * TC;
-    if constexpr (GROUPED) {
-        const RowTile rt = find_row_tile<QT>(g.offsets, g.G, g.M, blockIdx.x / tiles_n);
-        if (rt.grp < 0) return;
-        grp = rt.grp;
-        m0 = rt.lo;
-        m_end = rt.lo + QT < rt.hi ? rt.lo + QT : rt.hi;
-    } else {
-        m0 = (blockIdx.x / tiles_n) * QT;
-        m_end = m0 + QT < g.M ? m0 + QT : g.M;
-    }
-    const int8_t* B = g.b + grp * g.N * g.K;
-    const float* sb = g.sb + grp * g.N;
+    constexpr int STAGE = (MT_M + MT_N) * 128, COPIES = STAGE / 4096;            // copies of a wave
+    constexpr int NI = 2;                                                        // 16-row blocks of B a wave
+    __shared__ __attribute__((aligned(16))) uint8_t lds[DEPTH * STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t cols = SWIGLU ? g.N / 2 : g.N;
+    constexpr int TC = SWIGLU ? MT_N / 2 : MT_N;                                     // output columns of a tile
+    const Int8Tile tile = tile_of<MT_M, GROUPED>(g, (int)((cols + TC - 1) / TC));
+    if (tile.grp < 0) return;
+    const int64_t n0 = tile.n * TC;
+    const int8_t* B = g.b + (tile.grp * g.N + n0) * g.K;
 
-    uint4 ra[4], rb[4];
-    auto load_stage = [&](int64_t k0) {
+    // Copy c of a wave fills rows 32c + 8 wave .. + 7 of a stage (A's rows, then B's): lane l brings row l / 8 of them, the
+    // chunk that belongs at position l % 8. Rows of A behind the group's and bytes past K are a neighbour's or zeros: the
+    // outputs of the first are not stored, the second are masked in A.
+    const int K = (int)g.K;
+    const v4i rA = rows_rsrc(g.a + tile.m0 * g.K, g.M - tile.m0, g.K);
+    const v4i rB = rows_rsrc(SWIGLU && wave >= 2 ? B + cols * g.K : B, cols - n0, g.K);        // waves 2, 3 bring up rows
+    const int row = 8 * wave + (lane >> 3), chunk = 16 * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
+    const int a_off = row * K + chunk, b_off = (SWIGLU ? row & 15 : row) * K + chunk;
+    const uint32_t lds0 = lds_offset(&lds[1024 * wave]);
+    const int nk = (K + 127) / 128, begin = GROUPED ? 0 : first_step((uint32_t)tile.n, nk);
+    auto stage = [&](int s) { return s + begin < nk ? s + begin : s + begin - nk; };
+    auto copy = [&](int s, uint32_t slot) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = (tid >> 3) + 32 * j;
-            const int64_t kk = k0 + 16 * (tid & 7), ar = m0 + row, br = b_row<SWIGLU, 16>(n0, row, cols);
-            const bool b_ok = SWIGLU ? n0 + (row / 32) * 16 + row % 16 < cols : br < cols;
-            ra[j] = (ar < m_end && kk < g.K) ? *reinterpret_cast<const uint4*>(g.a + ar * g.K + kk) : make_uint4(0, 0, 0, 0);
-            rb[j] = (b_ok && kk < g.K) ? *reinterpret_cast<const uint4*>(B + br * g.K + kk) : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < COPIES; ++c) {
+            if (32 * c < MT_M) dma_to_lds<16>(rA, lds0 + slot + 4096 * c, a_off + 32 * c * K, stage(s) * 128);
+            else dma_to_lds<16>(rB, lds0 + slot + 4096 * c, b_off + (SWIGLU ? 16 : 32) * (c - MT_M / 32) * K, stage(s) * 128);
         }
     };
-    auto store_stage = [&](int buf) {
+    v4i acc[NI][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int row = (tid >> 3) + 32 * j;
-            *reinterpret_cast<uint4*>(&sA[buf][q_swz(row, tid & 7)]) = ra[j];
-            *reinterpret_cast<uint4*>(&sB[buf][q_swz(row, tid & 7)]) = rb[j];
-        }
-    };
-    v4i acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = v4i{0, 0, 0, 0};
     const int r16 = lane & 15, q16 = lane >> 4;
-    const int nk = (int)((g.K + QK - 1) / QK);
-    load_stage(0);
-    store_stage(0);
-    __syncthreads();
-    for (int kt = 0; kt < nk; ++kt) {
-        const int buf = kt & 1;
-        if (kt + 1 < nk) load_stage((int64_t)(kt + 1) * QK);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            v4i fa[4], fb[4];
+    for (int d = 0; d < DEPTH - 1; ++d)
+        if (d < nk) copy(d, d * STAGE);
+    uint32_t slot = 0;
+    for (int s = 0; s < nk; ++s) {
+        if (s + DEPTH - 2 < nk) wait_copies_barrier<(DEPTH - 2) * COPIES>();
+        else wait_copies_barrier<0>();
+        const uint32_t before = slot == 0 ? (DEPTH - 1) * STAGE : slot - STAGE;
+        if (s + DEPTH - 1 < nk) copy(s + DEPTH - 1, before);
+        const int left = K - 128 * stage(s);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int in_row = r16 * 128 + 16 * ((4 * u + q16) ^ (r16 >> 1));
+            v4i fa[4], fb[NI];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                fa[j] = *reinterpret_cast<const v4i*>(&sA[buf][q_swz(wm * 64 + j * 16 + r16, 4 * h + q16)]);
+                fa[j] = *reinterpret_cast<const v4i*>(&lds[slot + 16 * j * 128 + in_row]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                fb[i] = *reinterpret_cast<const v4i*>(&sB[buf][q_swz(wn * 64 + i * 16 + r16, 4 * h + q16)]);
+            for (int i = 0; i < NI; ++i)
+                fb[i] = *reinterpret_cast<const v4i*>(&lds[slot + (MT_M + 32 * wave + 16 * i) * 128 + in_row]);
+            if (left < 128) {
+                const int keep = 64 * u + 16 * q16 < left ? -1 : 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fa[j][e] &= keep;
+            }
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb[i], fa[j], acc[i][j], 0, 0, 0);
         }
-        if (kt + 1 < nk) store_stage(buf ^ 1);
-        __syncthreads();
+        slot = slot == (DEPTH - 1) * STAGE ? 0u : slot + STAGE;
     }
 
+    const float* sb = g.sb + tile.grp * g.N;
     const bool vec_ok = (g.ldc & 3) == 0 && (reinterpret_cast<uintptr_t>(g.c) & 7) == 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int64_t m = m0 + wm * 64 + j * 16 + r16;
-        if (m >= m_end) continue;
-        const float s = g.sa[m];
+        const int64_t m = tile.m0 + j * 16 + r16;
+        if (m >= tile.m_end) continue;
+        const float sa = g.sa[m];
 #pragma unroll
-        for (int i = 0; i < 4; i += SWIGLU ? 2 : 1) {
-            const int64_t n = SWIGLU ? n0 + wn * 32 + (i / 2) * 16 + 4 * q16 : n0 + wn * 64 + i * 16 + 4 * q16;
+        for (int i = 0; i < NI; i += SWIGLU ? 2 : 1) {
+            const int64_t n = n0 + (SWIGLU ? 16 * wave : 32 * wave + 16 * i) + 4 * q16;
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 if (n + e >= cols) {
                     v[e] = 0.0f;
                 } else if constexpr (SWIGLU) {
-                    v[e] = silu_times(int8_value(acc[i][j][e], s, sb[n + e]),
-                                      int8_value(acc[i + 1][j][e], s, sb[cols + n + e]));
+                    v[e] = silu_times(int8_value(acc[i][j][e], sa, sb[n + e]),
+                                      int8_value(acc[i + 1][j][e], sa, sb[cols + n + e]));
                 } else {
-                    v[e] = int8_value(acc[i][j][e], s, sb[n + e]);
+                    v[e] = int8_value(acc[i][j][e], sa, sb[n + e]);
                 }
+            }
+            uint16_t* dst = g.c + m * g.ldc + n;
+            if (vec_ok && n + 4 <= cols) {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (n + e < cols) dst[e] = (uint16_t)pack_bf16(v[e], 0.0f);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// One tile a CU: up to 16 MA tokens against `blocks` (at most MOST) 16-row blocks of B, a number that the host chooses so that the
+// workgroups are one for each CU, or as near to whole rounds of that as N allows: what a CU copies into LDS takes its time
+// whatever asks for it, so the CU with the most bytes decides. Stages of 128 bytes of K in a ring of DEPTH, rows of 128 bytes
+// swizzled as in the middle tiles, one barrier for PER stages. The waves share the tile's blocks (SwiGLU: its pairs of a gate
+// and an up block) in turn: all four a stage (PER = 1), or waves 0 and 1 the first of two stages and waves 2 and 3 the second,
+// and these hand their sums to the former at the end (PER = 2: a barrier's and the fragments' latency for twice the bytes, but
+// the ring runs two stages shorter: for tiles of few blocks, which leave room for a long ring; 61 tokens at 8192 x 8192 take
+// 20.7 us so and 34.7 with PER = 1, at 36864 x 12288 96 and 88). Every wave issues the same number of copies a stage, those
+// past the tile's blocks or past K for a place behind the operand, so that one count serves all waits.
+template <int MA, int MOST, int PER, int DEPTH, bool SWIGLU>
+__global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) {
+    constexpr int COPIES = (MA + MOST + 1) / 2, STAGE = 4096 * COPIES;
+    constexpr int SHARE = 4 / PER;                              // waves that share a stage's blocks
+    constexpr int NI = SWIGLU ? (MOST / 2 + SHARE - 1) / SHARE * 2 : MOST / SHARE;      // blocks of a wave
+    static_assert(PER == 1 || DEPTH * STAGE >= 2 * 64 * NI * MA * 16, "the ring holds two waves' sums");
+    __shared__ __attribute__((aligned(16))) uint8_t lds[DEPTH * STAGE];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t cols = SWIGLU ? g.N / 2 : g.N;
+    const int tc = SWIGLU ? 8 * blocks : 16 * blocks;           // output columns of a tile
+    const int tiles_m = (int)((g.M + 16 * MA - 1) / (16 * MA));
+    const int64_t m0 = (int64_t)(blockIdx.x % tiles_m) * (16 * MA), n0 = (int64_t)(blockIdx.x / tiles_m) * tc;
+    const int64_t m_end = m0 + 16 * MA < g.M ? m0 + 16 * MA : g.M;
+    const int8_t* B = g.b + n0 * g.K;
+    const int K = (int)g.K, nk = (K + 127) / 128;
+    const int begin = first_step((uint32_t)(n0 / tc), nk);
+    auto stage = [&](int s) { return s + begin < nk ? s + begin : s + begin - nk; };
+
+    // Copy j of a wave fills the 8 rows wave + 4j of a stage: A's 2 MA, then two for each block of B.
+    const bool up = SWIGLU && (((wave >> 1) + MA) & 1);         // whether the wave's B rows are up rows
+    const v4i rA = rows_rsrc(g.a + m0 * g.K, m_end - m0, g.K);
+    const v4i rB = rows_rsrc(up ? B + cols * g.K : B, cols - n0, g.K);
+    const uint32_t lds0 = lds_offset(&lds[1024 * wave]);
+    int off[COPIES];
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j) {
+        const int e = wave + 4 * j, b = (e - 2 * MA) >> 1;      // eight rows, block of B
+        const int row = e < 2 * MA ? 8 * e : 16 * (SWIGLU ? b / 2 : b) + 8 * (e & 1);
+        off[j] = (row + (lane >> 3)) * K + 16 * ((lane & 7) ^ (4 * (wave & 1) + (lane >> 4)));
+        if (e >= 2 * MA && b >= blocks) off[j] = 0x7FFFFFF0;
+    }
+    auto copy = [&](int s, uint32_t slot) {
+#pragma unroll
+        for (int j = 0; j < COPIES; ++j)
+            dma_to_lds<16>(wave + 4 * j < 2 * MA ? rA : rB, lds0 + slot + 4096 * j, s < nk ? off[j] : 0x7FFFFFF0,
+                           s < nk ? stage(s) * 128 : 0);
+    };
+    auto next = [](uint32_t slot) { return slot == (DEPTH - 1) * STAGE ? 0u : slot + STAGE; };
+    const int part = wave % SHARE, which = wave / SHARE;        // of the blocks, of a barrier's stages
+    auto block_of = [&](int x) { return SWIGLU ? 2 * (part + SHARE * (x >> 1)) + (x & 1) : part + SHARE * x; };
+    v4i acc[NI][MA];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int j = 0; j < MA; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+    const int r16 = lane & 15, q16 = lane >> 4;
+#pragma unroll
+    for (int d = 0; d < DEPTH - PER; ++d) copy(d, d * STAGE);
+    uint32_t slot = 0, into = (DEPTH - PER) * STAGE;
+    for (int s = 0; s < nk; s += PER) {
+        // the next PER stages have landed for every wave, and the PER before them have been read
+        wait_copies_barrier<(DEPTH - 2 * PER) * COPIES>();
+#pragma unroll
+        for (int d = 0; d < PER; ++d) {
+            copy(s + DEPTH - PER + d, into);
+            into = next(into);
+        }
+        const int mine = s + which;
+        const uint32_t at = which ? next(slot) : slot;
+        if (mine < nk) {
+            const int left = K - 128 * stage(mine);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int in_row = r16 * 128 + 16 * ((4 * u + q16) ^ (r16 >> 1));
+                v4i fa[MA];
+#pragma unroll
+                for (int j = 0; j < MA; ++j) fa[j] = *reinterpret_cast<const v4i*>(&lds[at + 16 * j * 128 + in_row]);
+                if (left < 128) {
+                    const int keep = 64 * u + 16 * q16 < left ? -1 : 0;
+#pragma unroll
+                    for (int j = 0; j < MA; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) fa[j][e] &= keep;
+                }
+#pragma unroll
+                for (int i = 0; i < NI; ++i) {
+                    if (block_of(i) < blocks) {
+                        const v4i fb = *reinterpret_cast<const v4i*>(&lds[at + 16 * (MA + block_of(i)) * 128 + in_row]);
+#pragma unroll
+                        for (int j = 0; j < MA; ++j)
+                            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(fb, fa[j], acc[i][j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        slot = PER == 2 ? next(next(slot)) : next(slot);
+    }
+    wait_copies_barrier<0>();                                   // no copy outlives the workgroup's LDS
+    if constexpr (PER == 2) {                                   // the second pair's sums, by way of the ring
+        v4i* sums = reinterpret_cast<v4i*>(lds) + part * (64 * NI * MA) + lane;
+        if (which) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int j = 0; j < MA; ++j) sums[64 * (i * MA + j)] = acc[i][j];
+        }
+        __syncthreads();
+        if (which) return;
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < MA; ++j) acc[i][j] += sums[64 * (i * MA + j)];
+    }
+    const bool vec_ok = (g.ldc & 3) == 0 && (reinterpret_cast<uintptr_t>(g.c) & 7) == 0;
+#pragma unroll
+    for (int i = 0; i < NI; i += SWIGLU ? 2 : 1) {
+        if (block_of(i) >= blocks) continue;
+        const int64_t n = n0 + (SWIGLU ? 8 : 16) * block_of(i) + 4 * q16;
+#pragma unroll
+        for (int j = 0; j < MA; ++j) {
+            const int64_t m = m0 + 16 * j + r16;
+            if (m >= m_end) continue;
+            const float sa = g.sa[m];
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (n + e >= cols) v[e] = 0.0f;
+                else if constexpr (SWIGLU) v[e] = silu_times(int8_value(acc[i][j][e], sa, g.sb[n + e]), int8_value(acc[i + 1][j][e], sa, g.sb[cols + n + e]));
+                else v[e] = int8_value(acc[i][j][e], sa, g.sb[n + e]);
             }
             uint16_t* dst = g.c + m * g.ldc + n;
             if (vec_ok && n + 4 <= cols) {
@@ -297,8 +481,6 @@ __global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Gemm g) {
 // region of p, trip 2p + 2 A's pair p + 3 into A's region of p. At the next barrier, behind trip 2p + 2, all but that last
 // pair of A must have landed: B has one to two trips to arrive, A three to four.
 constexpr int LT = 256, LK = 64, LPAIR = 2 * LK, LREGION = LT * LPAIR, LREGIONS_A = 3;
-constexpr int LGROUP_M = 4;            // row tiles that an XCD's workgroups walk together
-constexpr int64_t LXCD = 32;           // workgroups of one XCD at a time
 
 // acc += b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the instruction
 // another destination and copies results about in the loop. The operands' loads are waited for by the compiler; nothing
@@ -316,31 +498,9 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     const int wm = wave & 1, wn = wave >> 1;
     const int64_t cols = SWIGLU ? g.N / 2 : g.N;
     constexpr int TC = SWIGLU ? LT / 2 : LT;
-    const int tiles_n = (int)((cols + TC - 1) / TC);
-
-    // ------------------------------------------------------------------ tile
-    int64_t m0, m_end, n0, grp = 0;
-    if constexpr (GROUPED) {
-        // each XCD (every eighth workgroup) takes chunks of LXCD consecutive tiles, which share an expert's weights
-        const int64_t nb = gridDim.x, b = blockIdx.x, round = 8 * LXCD;
-        const int64_t t = b < (nb / round) * round ? (b >> 3) / LXCD * round + (b & 7) * LXCD + (b >> 3) % LXCD : b;
-        n0 = (t % tiles_n) * TC;
-        const RowTile rt = find_row_tile<LT>(g.offsets, g.G, g.M, t / tiles_n);
-        if (rt.grp < 0) return;
-        grp = rt.grp;
-        m0 = rt.lo;
-        m_end = rt.lo + LT < rt.hi ? rt.lo + LT : rt.hi;
-    } else {
-        // each XCD walks a contiguous run of an order in groups of LGROUP_M row tiles
-        const int tiles_m = (int)((g.M + LT - 1) / LT);
-        const int T = tiles_m * tiles_n, T8 = T & ~7, b = blockIdx.x;
-        const int v = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
-        const int per_group = LGROUP_M * tiles_n, first_m = (v / per_group) * LGROUP_M;
-        const int gm = min(LGROUP_M, tiles_m - first_m), r = v % per_group;
-        m0 = (int64_t)(first_m + r % gm) * LT;
-        n0 = (int64_t)(r / gm) * TC;
-        m_end = m0 + LT < g.M ? m0 + LT : g.M;
-    }
+    const Int8Tile tile = tile_of<LT, GROUPED>(g, (int)((cols + TC - 1) / TC));
+    if (tile.grp < 0) return;
+    const int64_t m0 = tile.m0, m_end = tile.m_end, n0 = tile.n * TC, grp = tile.grp;
     const int8_t* A = g.a + m0 * g.K;
     const int8_t* B = g.b + (grp * g.N + n0) * g.K;             // SwiGLU: the gate rows; the up rows are cols rows further
     const int64_t n_end = n0 + TC < cols ? n0 + TC : cols;
@@ -370,9 +530,8 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     // belongs at position l % 8. The resources end with the operand: rows behind its end are zeros, rows of A behind the
     // group's are the next group's, and what a last pair asks for past the end of K is a part of the next row (their
     // outputs are never stored, and the last is masked).
-    auto bytes = [&](int64_t rows) { return (uint32_t)(rows * g.K < 0x7FFFFFFF ? rows * g.K : 0x7FFFFFFF); };
-    const v4i rA = buffer_rsrc(A, bytes(g.M - m0));
-    const v4i rB = buffer_rsrc(SWIGLU && wave >= 2 ? B + cols * g.K : B, bytes(cols - n0));   // waves 2, 3 bring up rows
+    const v4i rA = rows_rsrc(A, g.M - m0, g.K);
+    const v4i rB = rows_rsrc(SWIGLU && wave >= 2 ? B + cols * g.K : B, cols - n0, g.K);        // waves 2, 3 bring up rows
     const int brow = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
     const int K = (int)g.K;
     const int a_off = brow * K + 16 * chunk, b_off = (SWIGLU ? brow & 15 : brow) * K + 16 * chunk;
@@ -554,25 +713,217 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     }
 }
 
+// ---------------------------------------------------------------------------------------------------------------
+// Few tokens: the work is reading the weights once. A workgroup takes 16 NT rows of B (SwiGLU: 16 gate rows and the up rows
+// of the same columns) for up to 16 MT tokens; its 4 waves share the contraction, 128 bytes of every row at a time, and each
+// runs on its own: a ring of DEPTH such steps in LDS, filled past the registers by copies of whole lines (8 rows of 128 bytes
+// an instruction; loads of 16 rows of 64 bytes, as the matrix instruction wants them, read at 3.5 to 4.8 TB/s where these
+// read at 5.7 to 6.5), rows of 128 bytes swizzled as in the large tiles. The waves' sums meet in LDS by integer additions,
+// whose order does not matter.
+constexpr int FEW_W = 4;
+template <int MT, int NT, int DEPTH, bool GROUPED, bool SWIGLU>
+__global__ __launch_bounds__(64 * FEW_W) void int8_few_kernel(Int8Gemm g) {
+    constexpr int W = FEW_W;
+    constexpr int STEP = 16 * (NT + MT) * 128, COPIES = STEP / 1024;
+    constexpr int PITCH = 16 * MT + 4;                          // words: the four row groups of a wave on banks of their own
+    __shared__ __attribute__((aligned(16))) uint8_t ring[W][DEPTH][STEP];
+    __shared__ int sums[16 * NT][PITCH];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t cols = SWIGLU ? g.N / 2 : g.N;
+    constexpr int TC = SWIGLU ? 8 * NT : 16 * NT;               // output columns of a workgroup
+    const int64_t tiles_n = (cols + TC - 1) / TC;
+    const int64_t n0 = (blockIdx.x % tiles_n) * TC;
+    int64_t m0, m_end, grp = 0;
+    if constexpr (GROUPED) {
+        const RowTile rt = find_row_tile<16 * MT>(g.offsets, g.G, g.M, blockIdx.x / tiles_n);
+        if (rt.grp < 0) return;
+        grp = rt.grp;
+        m0 = rt.lo;
+        m_end = rt.lo + 16 * MT < rt.hi ? rt.lo + 16 * MT : rt.hi;
+    } else {
+        m0 = (blockIdx.x / tiles_n) * (16 * MT);
+        m_end = m0 + 16 * MT < g.M ? m0 + 16 * MT : g.M;
+    }
+    const int rows = (int)(m_end - m0), K = (int)g.K;
+    const int r16 = lane & 15, q16 = lane >> 4;
+    for (int i = tid; i < 16 * NT * PITCH; i += 64 * W) (&sums[0][0])[i] = 0;
+
+    // The wave's steps are its pieces wave + W i of 128 bytes, from a place of the workgroup's own on. Copies of steps past the last ask for a place behind the operands.
+    // Rows behind an operand's end, and bytes past K, are zeros or a neighbour's: the sums of the first are not stored, the
+    // second are masked in A.
+    const int8_t* B = g.b + (grp * g.N + n0) * g.K;
+    const v4i rA = rows_rsrc(g.a + m0 * g.K, rows, g.K);
+    const v4i rB = rows_rsrc(B, cols - n0, g.K);
+    const v4i rU = SWIGLU ? rows_rsrc(B + cols * g.K, cols - n0, g.K) : rB;
+    const int pieces = (K + 127) / 128, steps = (pieces + W - 1 - wave) / W;
+    const int begin = GROUPED ? 0 : first_step((uint32_t)(n0 / TC), steps);
+    auto piece = [&](int s) { return wave + W * (s + begin < steps ? s + begin : s + begin - steps); };
+    const int at[2] = {(lane >> 3) * K + 16 * ((lane & 7) ^ (lane >> 4)), (lane >> 3) * K + 16 * ((lane & 7) ^ 4 ^ (lane >> 4))};
+    const uint32_t lds0 = lds_offset(&ring[wave][0][0]);
+    auto copy = [&](int s, uint32_t slot) {
+        const int k = s < steps ? 128 * piece(s) : 0x7F000000;
+#pragma unroll
+        for (int c = 0; c < COPIES; ++c) {
+            const int row = 8 * c;                              // of the ring: B's 16 NT, then A's
+            const bool b = row < 16 * NT;
+            const int r = !b ? row - 16 * NT : SWIGLU ? 16 * (row / 32) + row % 16 : row;
+            dma_to_lds<16>(!b ? rA : SWIGLU && (row & 16) ? rU : rB, lds0 + slot + 1024 * c, at[c & 1] + r * K + k, 0);
+        }
+    };
+    v4i acc[NT][MT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) copy(d, d * STEP);
+    uint32_t slot = 0;
+    for (int s = 0; s < steps; ++s) {
+        asm volatile("s_waitcnt vmcnt(%0)" :: "n"((DEPTH - 1) * COPIES) : "memory");    // step s has landed
+        v4i f[2][NT + MT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < NT + MT; ++i)
+                f[u][i] = *reinterpret_cast<const v4i*>(&ring[wave][0][slot + (16 * i + r16) * 128 + 16 * ((4 * u + q16) ^ (r16 >> 1))]);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");                              // and has been read
+        copy(s + DEPTH, slot);
+        slot = slot == (DEPTH - 1) * STEP ? 0u : slot + STEP;
+        const int left = K - 128 * piece(s);
+        if (left < 128) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int keep = 64 * u + 16 * q16 < left ? -1 : 0;
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) f[u][NT + j][e] &= keep;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f[u][i], f[u][NT + j], acc[i][j], 0, 0, 0);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");            // no copy outlives the workgroup's LDS
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) atomicAdd(&sums[16 * i + 4 * q16 + e][16 * j + r16], acc[i][j][e]);
+    __syncthreads();
+    const float* sb = g.sb + grp * g.N;
+    for (int i = tid; i < TC * rows; i += 64 * W) {
+        const int c = i % TC, m = i / TC;
+        if (n0 + c >= cols) continue;
+        const float sa = g.sa[m0 + m];
+        float v;
+        if constexpr (SWIGLU) {
+            const int r = 32 * (c / 16) + c % 16;
+            v = silu_times(int8_value(sums[r][m], sa, sb[n0 + c]), int8_value(sums[r + 16][m], sa, sb[cols + n0 + c]));
+        } else {
+            v = int8_value(sums[c][m], sa, sb[n0 + c]);
+        }
+        g.c[(m0 + m) * g.ldc + n0 + c] = (uint16_t)pack_bf16(v, 0.0f);
+    }
+}
+
 // Upper bound of the row tiles of TH rows over ragged groups: every group with rows adds at most one partial tile.
 static int64_t most_row_tiles(int64_t rows, int64_t G, int64_t TH) { return (rows + TH - 1) / TH + (G < rows ? G : rows); }
 
-// Large tiles where they fill the chip: at least 512 rows and output columns (grouped: 512 rows an expert on average).
-static bool large_tiles(int64_t M, int64_t cols, int64_t G) { return cols >= 512 && M >= 512 * (G ? G : 1); }
+// Which kernel takes a call, and its grid. The rules are on the rows of A (for each expert, on average) and on sizes that say how
+// many workgroups the middle tiles would make; the times are of one call, us, at rows x N x K.
+enum : int { INT8_FEW, INT8_WIDE, INT8_MIDDLE, INT8_LARGE };
+struct Int8Plan {
+    int kind, rows;             // rows of A in a tile
+    int wide;                   // 16-row blocks of B in a wide tile
+    bool deep;                  // middle tiles: the longer ring
+    int64_t blocks;
+};
 
-int64_t int8_gemm_blocks(int64_t M, int64_t cols, int64_t G, int swiglu) {
-    const int64_t tile = large_tiles(M, cols, G) ? LT : QT, tc = swiglu ? tile / 2 : tile;
-    const int64_t tiles_n = (cols + tc - 1) / tc, tiles_m = G ? most_row_tiles(M, G, tile) : (M + tile - 1) / tile;
-    return tiles_n > 0 && tiles_m > INT64_MAX / tiles_n ? INT64_MAX : tiles_m * tiles_n;
+static Int8Plan int8_plan(int64_t M, int64_t cols, int64_t K, int64_t G, bool swiglu) {
+    Int8Plan p{};
+    const int64_t groups = G ? G : 1, N = swiglu ? 2 * cols : cols;
+    auto count = [&](int64_t th, int64_t tc) {
+        const int64_t tn = (cols + tc - 1) / tc, tm = G ? most_row_tiles(M, G, th) : (M + th - 1) / th;
+        return tn > 0 && tm > INT64_MAX / tn ? INT64_MAX : tm * tn;
+    };
+    const int64_t middle = count(MT_M, swiglu ? MT_N / 2 : MT_N), weight = N * K;
+    // One dense pass over weights of 96 MB and more (128 MB for up to 32 tokens, 256 MB for up to 16, as fewer tokens leave less
+    // to share): wide tiles, where N makes two blocks a CU. Wide and few at 16 x 36864 x 12288: 79 and 90 us, 61 rows 88 and 132;
+    // at 32 x 12288 x 12288 32 and 38, 61 rows 40 and 50; but 16 rows 33 and 31, and at 61 x 8192 x 8192 21 and 15.
+    if (!G && M > 4 && M <= 128 && N >= 8192 && weight >= (M <= 16 ? 256000000 : M <= 32 ? 128000000 : 96000000)) {
+        p.kind = INT8_WIDE;
+        p.rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+        const int64_t units = (cols + 15) / 16;
+        int64_t best = INT64_MAX;
+        for (int k = 1; k <= (swiglu ? 6 : 12); ++k) {
+            const int b = swiglu ? 2 * k : k;
+            const int64_t cost = ((units + k - 1) / k + 255) / 256 * (b + p.rows / 16);
+            if (cost <= best) {
+                best = cost;
+                p.wide = b;
+            }
+        }
+        p.blocks = count(p.rows, (swiglu ? 8 : 16) * (int64_t)p.wide);
+    // Up to 8 rows an expert (64 dense ones), or so few middle tiles that half the CUs had none: the contraction is shared within
+    // a workgroup. Few and middle at 100 x 6144 x 2048: 11 and 13 us, 256 x 2048 x 8192 13 and 34, 200 x 6144 x 2048 17 and 14;
+    // 64 experts, up to 2048 x 2048 with SwiGLU: 16 rows an expert 65 and 60, 32 86 and 63.
+    } else if (M <= (G ? 8 * groups : 64) || middle <= 128) {
+        p.kind = INT8_FEW;
+        p.rows = M <= 16 * groups ? 16 : M <= 32 * groups ? 32 : 64;
+        p.blocks = count(p.rows, p.rows == 16 || swiglu ? 16 : 32);
+    // Three middle tiles a CU are as much as the large ones take for one round. Middle and large at 400 x 12288 x 12288: 117 and
+    // 122 us, 512 rows 129 and 124, 768 195 and 125, 160 x 36864 x 12288 176 and 149; 64 experts of 64 rows, up 70 and 77, of 88
+    // rows 85 and 78.
+    } else if (middle >= 768 && M >= 80 * groups) {
+        p.kind = INT8_LARGE;
+        p.rows = LT;
+        p.blocks = count(LT, swiglu ? LT / 2 : LT);
+    // Three stages, two workgroups a CU, while these hold all tiles; two stages, three workgroups, beyond: at 130 x 12288 x 12288
+    // 81 and 91 us, at 400 rows 142 and 117.
+    } else {
+        p.kind = INT8_MIDDLE;
+        p.rows = MT_M;
+        p.blocks = middle;
+        p.deep = middle <= 512;
+    }
+    return p;
+}
+
+bool int8_gemm_fits(int64_t M, int64_t cols, int64_t K, int64_t G, int swiglu) {
+    return int8_plan(M, cols, K, G, swiglu != 0).blocks <= kMaxThreads / 256;
+}
+
+template <int MOST, bool SWIGLU>
+static void launch_wide(const Int8Gemm& g, const Int8Plan& p, hipStream_t stream) {
+    const dim3 blocks((unsigned)p.blocks), threads(256);
+    constexpr bool S = MOST == 4;
+    constexpr int PER = S ? 2 : 1;
+    if (p.rows == 16) hipLaunchKernelGGL((int8_wide_kernel<1, MOST, PER, S ? 12 : 5, SWIGLU>), blocks, threads, 0, stream, g, p.wide);
+    else if (p.rows == 32) hipLaunchKernelGGL((int8_wide_kernel<2, MOST, PER, S ? 12 : 5, SWIGLU>), blocks, threads, 0, stream, g, p.wide);
+    else if (p.rows == 64) hipLaunchKernelGGL((int8_wide_kernel<4, MOST, PER, S ? 10 : 5, SWIGLU>), blocks, threads, 0, stream, g, p.wide);
+    else hipLaunchKernelGGL((int8_wide_kernel<8, MOST, PER, S ? 6 : 4, SWIGLU>), blocks, threads, 0, stream, g, p.wide);
 }
 
 template <bool GROUPED, bool SWIGLU>
 static void launch_products(const Int8Gemm& g, int64_t cols, hipStream_t stream) {
-    const dim3 blocks((unsigned)int8_gemm_blocks(g.M, cols, g.G, SWIGLU));
-    if (large_tiles(g.M, cols, g.G))
-        hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU>), blocks, dim3(256), 0, stream, g);
-    else
-        hipLaunchKernelGGL((int8_gemm_kernel<GROUPED, SWIGLU>), blocks, dim3(256), 0, stream, g);
+    const Int8Plan p = int8_plan(g.M, cols, g.K, g.G, SWIGLU);
+    const dim3 blocks((unsigned)p.blocks), threads(256);
+    if (p.kind == INT8_LARGE) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
+    else if (p.kind == INT8_MIDDLE && p.deep) hipLaunchKernelGGL((int8_gemm_kernel<3, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
+    else if (p.kind == INT8_MIDDLE) hipLaunchKernelGGL((int8_gemm_kernel<2, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
+    else if (p.kind == INT8_WIDE && p.wide <= 4) launch_wide<4, SWIGLU>(g, p, stream);
+    else if (p.kind == INT8_WIDE) launch_wide<12, SWIGLU>(g, p, stream);
+    else if (p.rows == 16) hipLaunchKernelGGL((int8_few_kernel<1, SWIGLU ? 2 : 1, 2, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
+    else if (p.rows == 32) hipLaunchKernelGGL((int8_few_kernel<2, 2, 2, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
+    else hipLaunchKernelGGL((int8_few_kernel<4, 2, 3, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
 }
 
 hipError_t launch_int8_gemm(const int8_t* a_q, const float* a_scale, const int64_t* offsets, int64_t G, int64_t M,

@@ -111,7 +111,7 @@ hipError_t launch_moe_few(const uint8_t* x_q, const uint8_t* x_s, const float* l
 int64_t int8_quantize_max_rows(int64_t cols);   // of one launch
 hipError_t launch_int8_quantize(const uint16_t* x, int64_t rows, int64_t cols, int8_t* q, float* scale,
                                 hipStream_t stream);
-int64_t int8_gemm_blocks(int64_t M, int64_t cols, int64_t G, int swiglu);   // workgroups of the largest grid a call uses
+bool int8_gemm_fits(int64_t M, int64_t cols, int64_t K, int64_t G, int swiglu);   // its tiles fit one launch
 hipError_t launch_int8_gemm(const int8_t* a_q, const float* a_scale, const int64_t* offsets, int64_t G, int64_t M,
                             const int8_t* b_q, const float* b_scale, int64_t N, int64_t K, int swiglu, uint16_t* c,
                             int64_t ldc, hipStream_t stream);

@@ -113,11 +113,19 @@ def _check(c, s, sa, sb, swiglu):
 
 SHAPES = [(1, 1, 32), (1, 6144, 2048), (2, 33, 96), (5, 130, 64), (16, 128, 1024), (17, 257, 160), (61, 1000, 544),
           (64, 256, 4096), (65, 96, 2080), (128, 384, 512), (130, 66, 12288), (200, 5000, 288), (257, 640, 1056),
-          (512, 512, 512), (700, 770, 1504), (1030, 1290, 2048), (1, 514, 36864), (300, 2050, 32)]
+          (512, 512, 512), (700, 770, 1504), (1030, 1290, 2048), (1, 514, 36864), (300, 2050, 32),
+          # middle tiles: both rings, contractions that end inside a line, one stage only
+          (130, 12300, 160), (130, 12290, 2048), (65, 16400, 32), (200, 20000, 288), (257, 16386, 96),
+          # large tiles: 1, 2, 3, 4 and more pairs of stages, ends of 32, 64 and 96 bytes, odd edges
+          (1030, 8200, 32), (1030, 8200, 64), (1030, 8200, 128), (1025, 8195, 160), (1030, 8200, 224), (1030, 8200, 288),
+          (1030, 8200, 384), (1030, 8200, 480), (1030, 8200, 512), (780, 16390, 1056), (2048, 4096, 4096)]
+# (rows, N, K) whose weights are large enough for one tile a CU, by token count
+WIDE = [(5, 20836, 12288), (16, 36864, 7008), (17, 10500, 12288), (32, 36866, 3488), (33, 8200, 12320), (64, 40000, 2400),
+        (61, 50000, 1952), (65, 8196, 12288), (100, 24580, 4000), (128, 36864, 2688)]
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
-@pytest.mark.parametrize("M,N,K", SHAPES)
+@pytest.mark.parametrize("M,N,K", SHAPES + WIDE)
 def test_dense(M, N, K, swiglu):
     if swiglu:
         N += N % 2
@@ -177,6 +185,11 @@ GROUPS = [
     (2, 1030, 2048, [0, 700, 1500]),
     (70, 40, 96, None),
     (1, 300, 96, [0, 33]),
+    (5, 4000, 160, [0, 100, 101, 101, 240, 300]),                         # middle tiles
+    (5, 4000, 96, [3, 400, 401, 500, 990, 1003]),
+    (3, 2060, 416, [0, 1, 1700, 3001]),                                   # large tiles
+    (9, 3000, 64, [0, 0, 255, 511, 767, 1023, 1400, 1401, 2200, 2200]),
+    (2, 4100, 544, [7, 7, 2000]),
 ]
 
 
@@ -188,7 +201,7 @@ def test_grouped(case, swiglu):
     g = _gen(case)
     if off is None:
         off = [0] + torch.cumsum(torch.randint(0, 5, (G,), generator=g, device=DEV), 0).tolist()
-    rows = off[-1] + (17 if case in (3, 4) else 0)
+    rows = off[-1] + (17 if case in (3, 4, 9, 12) else 0)
     a, sa, b, sb = _operands(g, rows, N, K, G)
     if swiglu:
         sa = sa * 0.001
@@ -216,12 +229,15 @@ def test_offsets_that_break_the_rule_write_nothing_astray(off):
 def test_a_row_does_not_depend_on_its_batch():
     """The sum is exact, so a token's row is the same bytes alone, in a batch, and in an expert's rows."""
     g = _gen(11)
-    a, sa, b, sb = _operands(g, 700, 512, 1024)
-    want = mxq.int8_scaled_gemm(a, sa, b, sb)
-    for m in (1, 16, 17, 64, 65, 300):
-        assert torch.equal(mxq.int8_scaled_gemm(a[:m], sa[:m], b, sb), want[:m])
-    off = torch.tensor([0, 200, 700], device=DEV)
-    assert torch.equal(mxq.int8_grouped_gemm(a, sa, off, torch.stack([b, b]), torch.stack([sb, sb])), want)
+    for N, K in ((512, 1024), (8320, 12288)):
+        a, sa, b, sb = _operands(g, 1300, N, K)
+        want = mxq.int8_scaled_gemm(a, sa, b, sb)
+        for m in (1, 16, 17, 64, 65, 100, 300):
+            assert torch.equal(mxq.int8_scaled_gemm(a[:m], sa[:m], b, sb), want[:m])
+            assert torch.equal(mxq.int8_scaled_gemm(a[9:9 + m], sa[9:9 + m], b, sb), want[9:9 + m])
+        off = torch.tensor([0, 200, 1300], device=DEV)
+        assert torch.equal(mxq.int8_grouped_gemm(a, sa, off, torch.stack([b, b]), torch.stack([sb, sb])), want)
+        assert torch.equal(mxq.int8_grouped_gemm(a[:9], sa[:9], off.clamp(max=9), torch.stack([b, b]), torch.stack([sb, sb])), want[:9])
 
 
 def test_products_past_32_bit_offsets():
