@@ -18,9 +18,9 @@ size_t pertensor_ws(int64_t n) { return round_up((size_t)mxq::pertensor_amax_par
 size_t adam_ws(int64_t n) { return round_up((size_t)mxq::adam_parts(n) * 4u, 256) + 256; }
 // One partial row of dgamma (cols floats) per workgroup of the backward.
 size_t rmsnorm_backward_ws(int64_t cols) { return round_up((size_t)mxq::kNormBwdParts * (size_t)cols * 4u, 256); }
-// One row of the dgamma sums of queries and keys (2 dim floats) per workgroup of the backward.
+// One row of dgamma sums (dim floats) per workgroup of the backward.
 size_t qk_norm_backward_ws(int64_t dim) {
-    return dim > mxq::kQkMaxDim ? 0 : round_up((size_t)mxq::kQkBwdParts * 2u * (size_t)dim * 4u, 256);
+    return dim > mxq::kQkMaxDim ? 0 : round_up((size_t)(mxq::kQkBwdParts + 1) * (size_t)dim * 4u, 256);
 }
 constexpr size_t kDelayedWs = 256;   // delayed modes: the atomic amax word (and Adam's three constants)
 constexpr int64_t kMaxHistory = 1 << 20;
@@ -40,6 +40,7 @@ mxq_status qk_args(const uint16_t* x, int64_t ld, int64_t tokens, int64_t hq, in
     if ((gamma_q == nullptr) != (gamma_k == nullptr)) return MXQ_ERR_NULL;
     if (gamma_q && !(eps > 0.0f && eps < 3.0e38f)) return MXQ_ERR_UNSUPPORTED;                  // NaN fails too
     if (tokens < 0 || tokens > (int64_t(1) << 25) || hq < 0 || hk < 0 || hq > 65536 || hk > 65536) return MXQ_ERR_SHAPE;
+    if (tokens * (hq + hk) > (int64_t(1) << 31)) return MXQ_ERR_SHAPE;                          // 32-bit counts of work
     if (dim < 16 || dim > mxq::kQkMaxDim || dim % 16 != 0 || rot < 0 || rot > dim || rot % 16 != 0) return MXQ_ERR_SHAPE;
     if (axes < 1 || axes > mxq::kQkMaxAxes) return MXQ_ERR_SHAPE;
     a = mxq::QkArgs{};
@@ -56,9 +57,17 @@ mxq_status qk_args(const uint16_t* x, int64_t ld, int64_t tokens, int64_t hq, in
         if (!al16(x) || !al16(gamma_q) || !al16(gamma_k) || !al16(q) || !al16(k)) return MXQ_ERR_ALIGN;
         if ((reinterpret_cast<uintptr_t>(positions) & 7u) || !al4(inv_freq)) return MXQ_ERR_ALIGN;
     }
-    a.x = x; a.ldx = ld; a.tokens = tokens; a.gamma_q = gamma_q; a.gamma_k = gamma_k; a.positions = positions;
-    a.inv_freq = inv_freq; a.q = q; a.k = k; a.q_token = q_token; a.q_head = q_head; a.k_token = k_token; a.k_head = k_head;
-    a.eps = eps; a.hq = (int)hq; a.hk = (int)hk; a.dim = (int)dim; a.rot = (int)rot; a.interleaved = interleaved != 0;
+    a.x = x;
+    a.ldx = ld;
+    a.tokens = tokens;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.kind[0] = mxq::QkKind{gamma_q, q, q_token, q_head, 0, (int)hq, 0, 0, 0, 0, 0};
+    a.kind[1] = mxq::QkKind{gamma_k, k, k_token, k_head, hq * dim, (int)hk, 0, 0, 0, 0, 0};
+    a.eps = eps;
+    a.dim = (int)dim;
+    a.rot = (int)rot;
+    a.interleaved = interleaved != 0;
     return MXQ_OK;
 }
 

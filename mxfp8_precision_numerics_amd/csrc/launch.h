@@ -119,23 +119,28 @@ hipError_t launch_int8_gemm(const int8_t* a_q, const float* a_scale, const int64
 // Head norms with the rotation by position (qk_norm.hip). In the backward q and k are the gradients of the outputs.
 constexpr int64_t kQkMaxDim = 256;
 constexpr int64_t kQkMaxAxes = 4;
-constexpr int64_t kQkBwdParts = 1024;
+constexpr int64_t kQkBwdParts = 512;        // rows of dgamma sums, and one more where a kind has few of them
+struct QkKind {                             // queries or keys
+    const float* gamma;                     // NULL: no norm
+    uint16_t* y;                            // the output; in the backward its gradient, which is only read
+    int64_t token, head;                    // strides of y
+    int64_t column;                         // of the kind's first head in a row of x
+    int heads;
+    int blocks, splits, per_item, groups;   // these and items: set by the launchers
+    uint32_t items;
+};
 struct QkArgs {
-    const uint16_t* x;                      // [tokens][ldx]: hq query heads, then hk key heads, of dim values
+    const uint16_t* x;                      // [tokens][ldx]: query heads, then key heads, of dim values
     int64_t ldx, tokens;
-    const float *gamma_q, *gamma_k;         // NULL: no norm
     const int64_t* positions;               // [axes][tokens]
     const float* inv_freq;                  // [rot / 2]
-    uint16_t *q, *k;
-    int64_t q_token, q_head, k_token, k_head;
+    QkKind kind[2];
     uint16_t* dx;                           // backward: [tokens][lddx], laid out like x
     int64_t lddx;
-    float* partial;                         // backward: a row of 2 dim sums for each workgroup
-    float eps, inv_dim;                     // inv_dim: set by the launchers, as the last five are
-    int hq, hk, dim, rot, interleaved;
+    float* partial;                         // backward: a row of dim sums for each workgroup
+    float eps, inv_dim;                     // inv_dim: set by the launchers
+    int dim, rot, interleaved;
     uint32_t axis[8];                       // 2 bits a pair
-    int q_blocks, k_blocks, splits, per_item;
-    int64_t items;
 };
 hipError_t launch_qk_forward(QkArgs a, hipStream_t stream);
 hipError_t launch_qk_backward(QkArgs a, float* dgamma_q, float* dgamma_k, int accumulate, hipStream_t stream);

@@ -12,6 +12,8 @@
 // are log2 P lane exchanges, and a wave takes 64 / P heads of one token at once. An angle depends on the token and the pair
 // alone: a wave computes a token's angles once, one pair a lane, and keeps them for all of the token's heads it takes.
 #pragma clang fp contract(off)
+#include <type_traits>
+
 #include "launch.h"
 #include "mx_block.h"
 
@@ -111,11 +113,16 @@ __device__ __forceinline__ void turn(float (&v)[16], const float (&c)[8], const 
     else turn_pairs<false>(v, c, s, sign);
 }
 
-// Sum over the P lanes of a head.
+// Sum over the P lanes of a head, by lane permutations within 16 lanes; every lane gets the same result.
 template <int P>
 __device__ __forceinline__ float head_sum(float v) {
-#pragma unroll
-    for (int o = 1; o < P; o <<= 1) v += __shfl_xor(v, o, 64);
+    auto add = [&](auto ctrl) {
+        v += __uint_as_float((uint32_t)__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), decltype(ctrl)::value, 0xF, 0xF, false));
+    };
+    if constexpr (P > 1) add(std::integral_constant<int, 0xB1>{});       // lane ^ 1
+    if constexpr (P > 2) add(std::integral_constant<int, 0x4E>{});       // lane ^ 2
+    if constexpr (P > 4) add(std::integral_constant<int, 0x141>{});      // the other four of eight
+    if constexpr (P > 8) add(std::integral_constant<int, 0x140>{});      // the other eight of sixteen
     return v;
 }
 
@@ -126,17 +133,25 @@ __device__ __forceinline__ float sum_squares16(const float (&v)[16]) {
     return tree_sum(q);
 }
 
-__device__ __forceinline__ void load16(const uint16_t* lo, const uint16_t* hi, bool ok, float (&v)[16]) {
+// A lane's two chunks as they lie in memory. Each value is used once: the loads and stores pass the caches by.
+struct Raw {
+    uint4 lo, hi;
+};
+__device__ __forceinline__ Raw load_raw(const uint16_t* lo, const uint16_t* hi, bool ok) {
     const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 a = ok ? *reinterpret_cast<const uint4*>(lo) : z, b = ok ? *reinterpret_cast<const uint4*>(hi) : z;
-    float x[8], y[8];
-    unpack8(a, x);
-    unpack8(b, y);
+    return Raw{ok ? ldnt16(lo) : z, ok ? ldnt16(hi) : z};
+}
+
+// Value e (0 .. 15) of them.
+__device__ __forceinline__ float value_of(const Raw& r, int e) {
+    const uint4& q = e < 8 ? r.lo : r.hi;
+    const uint32_t w = (e & 7) < 2 ? q.x : (e & 7) < 4 ? q.y : (e & 7) < 6 ? q.z : q.w;
+    return (e & 1) ? bf16_hi(w) : bf16_lo(w);
+}
+
+__device__ __forceinline__ void unpack16(const Raw& r, float (&v)[16]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        v[e] = x[e];
-        v[8 + e] = y[e];
-    }
+    for (int e = 0; e < 16; ++e) v[e] = value_of(r, e);
 }
 
 __device__ __forceinline__ void store16(uint16_t* lo, uint16_t* hi, const float (&v)[16]) {
@@ -146,8 +161,8 @@ __device__ __forceinline__ void store16(uint16_t* lo, uint16_t* hi, const float 
         x[e] = v[e];
         y[e] = v[8 + e];
     }
-    *reinterpret_cast<uint4*>(lo) = pack8(x);
-    *reinterpret_cast<uint4*>(hi) = pack8(y);
+    stnt16(lo, pack8(x));
+    stnt16(hi, pack8(y));
 }
 
 __device__ __forceinline__ void load_gamma16(const float* g, const Unit& un, float (&v)[16]) {
@@ -159,181 +174,216 @@ __device__ __forceinline__ void load_gamma16(const float* g, const Unit& un, flo
     }
 }
 
-// A wave's work: blocks [first, last) of 64 / P heads of one token, the query blocks ahead of the key blocks.
+// A workgroup takes queries or keys; its waves' items are runs of blocks of 64 / P heads of one token, each wave every
+// (4 groups)-th item of the kind.
 struct Item {
     int64_t token;
-    int first, last;
+    int first, last;            // blocks
 };
 
-__device__ __forceinline__ Item item_of(const QkArgs& a, int64_t i) {
+__device__ __forceinline__ Item item_of(const QkKind& k, uint32_t i) {
     Item r;
-    r.token = i / a.splits;
-    r.first = (int)(i - r.token * a.splits) * a.per_item;
-    r.last = min(r.first + a.per_item, a.q_blocks + a.k_blocks);
+    const uint32_t t = i / (uint32_t)k.splits;
+    r.token = t;
+    r.first = (int)(i - t * k.splits) * k.per_item;
+    r.last = min(r.first + k.per_item, k.blocks);
     return r;
 }
 
+// Bound by memory, 4 bytes a value: 4096 tokens of 96 + 96 heads of 128 in 69.3 us, 5.8 TB/s. The next block's values are on
+// their way while a block is at work.
 template <int P, bool NORM>
 __global__ __launch_bounds__(256) void qk_forward_kernel(QkArgs a) {
     __shared__ __attribute__((aligned(16))) float2 angles[4][8 * P];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     constexpr int HEADS = 64 / P;
     const Unit un = unit_of<P>(a, lane % P);
-    const int64_t at = (int64_t)blockIdx.x * 4 + wave;
-    if (at >= a.items) return;
-    const Item it = item_of(a, at);
-    float c[8], s[8];
-    token_angles<P>(a, it.token, lane, un, angles[wave], c, s);
+    const int kind = (int)blockIdx.x >= a.kind[0].groups;
+    const QkKind k = a.kind[kind];
+    const int group = (int)blockIdx.x - (kind ? a.kind[0].groups : 0), slot = lane / P;
     float gamma[16];
-    int loaded = -1;
-    for (int b = it.first; b < it.last; ++b) {
-        const bool is_k = b >= a.q_blocks;
-        const int head = (is_k ? b - a.q_blocks : b) * HEADS + lane / P;
-        const bool ok = un.on && head < (is_k ? a.hk : a.hq);
-        if (NORM && loaded != (int)is_k) {
-            load_gamma16(is_k ? a.gamma_k : a.gamma_q, un, gamma);
-            loaded = is_k;
-        }
-        const uint16_t* x = a.x + it.token * a.ldx + (int64_t)((is_k ? a.hq : 0) + head) * a.dim;
-        float v[16];
-        load16(x + un.lo, x + un.hi, ok, v);
-        if constexpr (NORM) {
-            const float ss = head_sum<P>(sum_squares16(v));
-            const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_dim, a.eps));
+    if constexpr (NORM) load_gamma16(k.gamma, un, gamma);
+    for (uint32_t at = 4 * group + wave; at < k.items; at += 4 * k.groups) {
+        const Item it = item_of(k, at);
+        const uint16_t* x = a.x + it.token * a.ldx + k.column + (int64_t)slot * a.dim;
+        uint16_t* y = k.y + it.token * k.token + (int64_t)slot * k.head;
+        auto load = [&](int b) {
+            const uint16_t* p = x + (int64_t)b * HEADS * a.dim;
+            return load_raw(p + un.lo, p + un.hi, un.on && b * HEADS + slot < k.heads && b < it.last);
+        };
+        Raw next = load(it.first);
+        float c[8], s[8];
+        token_angles<P>(a, it.token, lane, un, angles[wave], c, s);
+        for (int b = it.first; b < it.last; ++b) {
+            float v[16];
+            unpack16(next, v);
+            next = load(b + 1);
+            if constexpr (NORM) {
+                const float ss = head_sum<P>(sum_squares16(v));
+                const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_dim, a.eps));
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = (v[e] * rstd) * gamma[e];
-        }
-        turn(v, c, s, un, a.interleaved, 1.0f);
-        if (ok) {
-            uint16_t* y = is_k ? a.k + it.token * a.k_token + (int64_t)head * a.k_head
-                               : a.q + it.token * a.q_token + (int64_t)head * a.q_head;
-            store16(y + un.lo, y + un.hi, v);
+                for (int e = 0; e < 16; ++e) v[e] = (v[e] * rstd) * gamma[e];
+            }
+            turn(v, c, s, un, a.interleaved, 1.0f);
+            if (un.on && b * HEADS + slot < k.heads) {
+                uint16_t* p = y + (int64_t)b * HEADS * k.head;
+                store16(p + un.lo, p + un.hi, v);
+            }
         }
     }
 }
 
-// The gradients; with dgamma asked for (partial != NULL) every workgroup leaves one row of 2 D sums (queries, keys). A
-// wave's items are every (4 gridDim)-th, so the sums are formed in a fixed order.
+// The gradients; with dgamma asked for (partial != NULL) every workgroup leaves one row of D sums. A wave's items follow
+// from its place alone, so the sums are formed in a fixed order. Bound by memory, 6 bytes a value: 4096 tokens of 96 + 96 heads of 128
+// in 113 us with the launch that joins the rows, 5.3 TB/s.
 template <int P, bool NORM>
 __global__ __launch_bounds__(256) void qk_backward_kernel(QkArgs a) {
     __shared__ __attribute__((aligned(16))) float2 angles[4][8 * P];
-    __shared__ float sums[4][2][16 * P];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ float sums[4][16 * P];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     constexpr int HEADS = 64 / P;
     const Unit un = unit_of<P>(a, lane % P);
-    float dg[2][16];
+    const int kind = (int)blockIdx.x >= a.kind[0].groups;
+    const QkKind k = a.kind[kind];
+    const int group = (int)blockIdx.x - (kind ? a.kind[0].groups : 0), slot = lane / P;
+    float gamma[16], dg[16];
+    if constexpr (NORM) load_gamma16(k.gamma, un, gamma);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) dg[0][e] = dg[1][e] = 0.0f;
-    for (int64_t at = (int64_t)blockIdx.x * 4 + wave; at < a.items; at += 4 * (int64_t)gridDim.x) {
-        const Item it = item_of(a, at);
+    for (int e = 0; e < 16; ++e) dg[e] = 0.0f;
+    for (uint32_t at = 4 * group + wave; at < k.items; at += 4 * k.groups) {
+        const Item it = item_of(k, at);
+        const uint16_t* dy = k.y + it.token * k.token + (int64_t)slot * k.head;
+        const uint16_t* xs = a.x + it.token * a.ldx + k.column + (int64_t)slot * a.dim;
+        uint16_t* dx = a.dx + it.token * a.lddx + k.column + (int64_t)slot * a.dim;
+        auto there = [&](int b) { return un.on && b * HEADS + slot < k.heads && b < it.last; };
+        auto load_dy = [&](int b) {
+            const uint16_t* p = dy + (int64_t)b * HEADS * k.head;
+            return load_raw(p + un.lo, p + un.hi, there(b));
+        };
+        auto load_x = [&](int b) {
+            const uint16_t* p = xs + (int64_t)b * HEADS * a.dim;
+            return load_raw(p + un.lo, p + un.hi, there(b));
+        };
+        Raw next_dy = load_dy(it.first), next_x;
+        if constexpr (NORM) next_x = load_x(it.first);
         float c[8], s[8];
         token_angles<P>(a, it.token, lane, un, angles[wave], c, s);
-        auto heads = [&](auto is_k_c, int first, int last) {
-            constexpr bool is_k = decltype(is_k_c)::value;
-            if (first >= last) return;
-            float gamma[16];
-            if constexpr (NORM) load_gamma16(is_k ? a.gamma_k : a.gamma_q, un, gamma);
-            for (int b = first; b < last; ++b) {
-                const int head = b * HEADS + lane / P;
-                const bool ok = un.on && head < (is_k ? a.hk : a.hq);
-                const uint16_t* dy = is_k ? a.k + it.token * a.k_token + (int64_t)head * a.k_head
-                                          : a.q + it.token * a.q_token + (int64_t)head * a.q_head;
-                const int64_t col = (int64_t)((is_k ? a.hq : 0) + head) * a.dim;
-                float d[16];
-                load16(dy + un.lo, dy + un.hi, ok, d);
-                float x[16];
-                if constexpr (NORM) load16(a.x + it.token * a.ldx + col + un.lo, a.x + it.token * a.ldx + col + un.hi, ok, x);
-                turn(d, c, s, un, a.interleaved, -1.0f);
-                if constexpr (NORM) {
-                    const float ss = head_sum<P>(sum_squares16(x));
-                    const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_dim, a.eps));
-                    float m[16];
+        for (int b = it.first; b < it.last; ++b) {
+            float d[16];
+            unpack16(next_dy, d);
+            next_dy = load_dy(b + 1);
+            turn(d, c, s, un, a.interleaved, -1.0f);
+            if constexpr (NORM) {
+                // both sums over the head are of the values as they came: sum t xh = rstd sum t x
+                const Raw now = next_x;
+                next_x = load_x(b + 1);
+                float sq[4] = {0.0f, 0.0f, 0.0f, 0.0f}, tx[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        x[e] = x[e] * rstd;
-                        dg[is_k][e] += d[e] * x[e];
-                        d[e] = d[e] * gamma[e];
-                        m[e] = d[e] * x[e];
-                    }
-                    const float mean = head_sum<P>(tree_sum(m)) * a.inv_dim;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) d[e] = rstd * (d[e] - x[e] * mean);
+                for (int e = 0; e < 16; ++e) {
+                    const float x = value_of(now, e);
+                    sq[e & 3] = __builtin_fmaf(x, x, sq[e & 3]);
+                    tx[e & 3] = __builtin_fmaf(d[e] * gamma[e], x, tx[e & 3]);
                 }
-                if (ok) {
-                    uint16_t* dx = a.dx + it.token * a.lddx + col;
-                    store16(dx + un.lo, dx + un.hi, d);
+                const float ss = head_sum<P>(tree_sum(sq)), st = head_sum<P>(tree_sum(tx));
+                const float rstd = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, a.inv_dim, a.eps)), mean = (st * a.inv_dim) * rstd;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float xh = value_of(now, e) * rstd;
+                    dg[e] = __builtin_fmaf(d[e], xh, dg[e]);
+                    d[e] = rstd * __builtin_fmaf(-xh, mean, d[e] * gamma[e]);
                 }
             }
-        };
-        heads(std::false_type{}, it.first, min(it.last, a.q_blocks));
-        heads(std::true_type{}, max(it.first, a.q_blocks) - a.q_blocks, it.last - a.q_blocks);
+            if (there(b)) {
+                uint16_t* p = dx + (int64_t)b * HEADS * a.dim;
+                store16(p + un.lo, p + un.hi, d);
+            }
+        }
     }
     if constexpr (NORM) {
         if (a.partial == nullptr) return;
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int e = 0; e < 16; ++e) {
+            float v = dg[e];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float v = dg[k][e];
-#pragma unroll
-                for (int o = P; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
-                if (lane < P && un.on) sums[wave][k][(e < 8 ? un.lo : un.hi) + (e & 7)] = v;
-            }
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * a.dim; i += 256) {
-            const int k = i >= a.dim, d = k ? i - a.dim : i;
-            a.partial[(int64_t)blockIdx.x * 2 * a.dim + i] = (sums[0][k][d] + sums[1][k][d]) + (sums[2][k][d] + sums[3][k][d]);
+            for (int o = P; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+            if (lane < P && un.on) sums[wave][(e < 8 ? un.lo : un.hi) + (e & 7)] = v;
         }
+        __syncthreads();
+        for (int i = threadIdx.x; i < a.dim; i += 256)
+            a.partial[(int64_t)blockIdx.x * a.dim + i] = (sums[0][i] + sums[1][i]) + (sums[2][i] + sums[3][i]);
     }
 }
 
-// dgamma from the workgroups' rows: 16 threads a column take every sixteenth row in 64 bits, joined in a fixed order.
-__global__ __launch_bounds__(256) void qk_dgamma_kernel(const float* __restrict__ partial, int parts, int dim,
-                                                       float* __restrict__ dq, float* __restrict__ dk, int accumulate) {
-    __shared__ double s[16][16];
-    const int col = blockIdx.x * 16 + (threadIdx.x & 15), part = threadIdx.x >> 4;
+// dgamma of queries (blockIdx.y = 0) or keys from the workgroups' rows: 64 threads a column take every 64th row in 64 bits, eight
+// loads in flight, joined in a fixed order.
+__global__ __launch_bounds__(1024) void qk_dgamma_kernel(const float* __restrict__ partial, int parts_q, int parts_k, int dim,
+                                                        float* __restrict__ dq, float* __restrict__ dk, int accumulate) {
+    __shared__ double s[64][17];
+    const int c = threadIdx.x & 15, part = threadIdx.x >> 4;
+    const int first = blockIdx.y ? parts_q : 0, rows = blockIdx.y ? parts_k : parts_q;
+    const float* p = partial + (int64_t)first * dim + blockIdx.x * 16 + c;
     double v = 0.0;
-    for (int p = part; p < parts; p += 16) v += (double)partial[(int64_t)p * 2 * dim + col];
-    s[part][threadIdx.x & 15] = v;
-    __syncthreads();
-    if (part == 0) {
-        double x[16];
+    for (int r = part; r < rows; r += 8 * 64) {
+        float x[8];
 #pragma unroll
-        for (int p = 0; p < 16; ++p) x[p] = s[p][threadIdx.x];
-        const double total = tree_sum(x);
-        float* out = col < dim ? dq + col : dk + (col - dim);
+        for (int i = 0; i < 8; ++i) x[i] = r + 64 * i < rows ? p[(int64_t)(r + 64 * i) * dim] : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v += (double)x[i];
+    }
+    s[part][c] = v;
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        double total = 0.0;
+#pragma unroll
+        for (int i = 0; i < 64; i += 16) {
+            double x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = s[i + j][c];
+            total += tree_sum(x);
+        }
+        float* out = (blockIdx.y ? dk : dq) + blockIdx.x * 16 + c;
         *out = (float)(accumulate ? (double)*out + total : total);
     }
 }
 
 namespace {
 
-constexpr int64_t kWaves = 8192;          // a launch with fewer waves leaves the chip's memory queues empty
-
 int lanes_per_head(int64_t dim) { return dim <= 64 ? (dim <= 16 ? 1 : dim <= 32 ? 2 : 4) : dim <= 128 ? 8 : 16; }
 
-// Items: a token's head blocks in runs of per_item, as long as there are waves enough.
-void split(QkArgs& a) {
+// Items: a token's head blocks of a kind in runs of up to 4, shorter ones while there are few tokens; workgroups: one for four
+// items, up to `most` of both kinds together, divided by their blocks. Measured at 4096 tokens of 96 + 96 heads of 128: the
+// forward takes 69.3 us with runs of 4 and up to 4096 workgroups, 71 to 74 with runs of 2 or 3, 76 to 83 with runs of 6 or 12 or
+// no more workgroups than the chip holds at once (each workgroup's own stretch of memory is then short and is read in order).
+// The backward keeps sums in registers and leaves a row for every workgroup: two of them a CU, all it holds, 113 us; 768 134,
+// 1024 117.
+constexpr int64_t kRun = 4, kForwardGroups = 4096;
+
+void split(QkArgs& a, int64_t most) {
     const int heads = 64 / lanes_per_head(a.dim);
-    a.q_blocks = (a.hq + heads - 1) / heads;
-    a.k_blocks = (a.hk + heads - 1) / heads;
-    const int64_t blocks = a.q_blocks + a.k_blocks;
     a.inv_dim = 1.0f / (float)a.dim;
-    if (a.tokens == 0 || blocks == 0) {
-        a.splits = a.per_item = 1;
-        a.items = 0;
-        return;
+    int64_t blocks = 0;
+    for (QkKind& k : a.kind) {
+        k.blocks = (k.heads + heads - 1) / heads;
+        blocks += k.blocks;
     }
-    int64_t per = a.tokens * blocks / kWaves;
-    per = per < 1 ? 1 : per > blocks ? blocks : per;
-    a.splits = (int)((blocks + per - 1) / per);
-    a.per_item = (int)((blocks + a.splits - 1) / a.splits);
-    a.items = a.tokens * a.splits;
+    for (QkKind& k : a.kind) {
+        k.splits = k.per_item = 1;
+        k.items = 0;
+        k.groups = 0;
+        if (a.tokens == 0 || k.blocks == 0) continue;
+        int64_t per = a.tokens * blocks / 8192;
+        per = per < 1 ? 1 : per > kRun ? kRun : per;
+        k.splits = (int)((k.blocks + per - 1) / per);
+        k.per_item = (k.blocks + k.splits - 1) / k.splits;
+        k.items = (uint32_t)(a.tokens * k.splits);
+        const int64_t want = ((int64_t)k.items + 3) / 4, share = most * k.blocks / blocks;
+        k.groups = (int)(want < share ? want : share < 1 ? 1 : share);
+    }
 }
 
 template <bool NORM>
 void forward(const QkArgs& a, hipStream_t stream) {
-    const dim3 grid((unsigned)((a.items + 3) / 4)), block(256);
+    const dim3 grid((unsigned)(a.kind[0].groups + a.kind[1].groups)), block(256);
     switch (lanes_per_head(a.dim)) {
         case 1: hipLaunchKernelGGL((qk_forward_kernel<1, NORM>), grid, block, 0, stream, a); break;
         case 2: hipLaunchKernelGGL((qk_forward_kernel<2, NORM>), grid, block, 0, stream, a); break;
@@ -344,8 +394,8 @@ void forward(const QkArgs& a, hipStream_t stream) {
 }
 
 template <bool NORM>
-void backward(const QkArgs& a, int64_t blocks, hipStream_t stream) {
-    const dim3 grid((unsigned)blocks), block(256);
+void backward(const QkArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)(a.kind[0].groups + a.kind[1].groups)), block(256);
     switch (lanes_per_head(a.dim)) {
         case 1: hipLaunchKernelGGL((qk_backward_kernel<1, NORM>), grid, block, 0, stream, a); break;
         case 2: hipLaunchKernelGGL((qk_backward_kernel<2, NORM>), grid, block, 0, stream, a); break;
@@ -358,23 +408,21 @@ void backward(const QkArgs& a, int64_t blocks, hipStream_t stream) {
 }  // namespace
 
 hipError_t launch_qk_forward(QkArgs a, hipStream_t stream) {
-    split(a);
-    if (a.gamma_q) forward<true>(a, stream);
+    split(a, kForwardGroups);
+    if (a.kind[0].gamma) forward<true>(a, stream);
     else forward<false>(a, stream);
     return hipGetLastError();
 }
 
 hipError_t launch_qk_backward(QkArgs a, float* dgamma_q, float* dgamma_k, int accumulate, hipStream_t stream) {
-    split(a);
-    int64_t blocks = (a.items + 3) / 4;
-    if (blocks > kQkBwdParts) blocks = kQkBwdParts;
-    if (blocks > 0) {
-        if (a.gamma_q) backward<true>(a, blocks, stream);
-        else backward<false>(a, blocks, stream);
+    split(a, kQkBwdParts);
+    if (a.kind[0].groups + a.kind[1].groups > 0) {
+        if (a.kind[0].gamma) backward<true>(a, stream);
+        else backward<false>(a, stream);
     }
     if (dgamma_q)
-        hipLaunchKernelGGL(qk_dgamma_kernel, dim3((unsigned)(2 * a.dim / 16)), dim3(256), 0, stream, a.partial, (int)blocks,
-                           a.dim, dgamma_q, dgamma_k, accumulate);
+        hipLaunchKernelGGL(qk_dgamma_kernel, dim3((unsigned)(a.dim / 16), 2), dim3(1024), 0, stream, a.partial,
+                           a.kind[0].groups, a.kind[1].groups, a.dim, dgamma_q, dgamma_k, accumulate);
     return hipGetLastError();
 }
 
