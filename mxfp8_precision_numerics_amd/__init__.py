@@ -27,6 +27,7 @@ outputs, and call the C ABI of libmxq.so with raw pointers. All arithmetic happe
 from __future__ import annotations
 
 import ctypes as C
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -677,15 +678,19 @@ class Int8Tensor(NamedTuple):
     scale: torch.Tensor                 # float32[rows]
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _checked(dev: torch.device, name: str, *args):
     """Calls the library with `dev` as the current device, on its current stream."""
     fn = getattr(_lib.load(), name)
-    if dev.index is None or dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():
         st = fn(*args, _here(dev))
     else:
         with torch.cuda.device(dev):
             st = fn(*args, _here(dev))
-    _lib.check(name, st)
+    if st:
+        _lib.check(name, st)
 
 
 def int8_quantize_tokens(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> Int8Tensor:
@@ -697,8 +702,7 @@ def int8_quantize_tokens(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> I
     rows, cols = x.shape
     dev = x.device
     if out is None:
-        out = Int8Tensor(torch.empty((rows, cols), dtype=torch.int8, device=dev),
-                         torch.empty(rows, dtype=torch.float32, device=dev))
+        out = Int8Tensor(x.new_empty((rows, cols), dtype=torch.int8), x.new_empty(rows, dtype=torch.float32))
     else:
         _expect(out.q, (rows, cols), torch.int8, dev, "out.q")
         _expect(out.scale, (rows,), torch.float32, dev, "out.scale")
@@ -706,10 +710,8 @@ def int8_quantize_tokens(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> I
     return out
 
 
-def _rows_out(out: Optional[torch.Tensor], rows: int, cols: int, dev) -> torch.Tensor:
-    """A new bf16 [rows][cols], or the caller's: its rows may be further apart."""
-    if out is None:
-        return torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+def _rows_out(out: torch.Tensor, rows: int, cols: int, dev) -> torch.Tensor:
+    """The caller's bf16 [rows][cols], whose rows may be further apart."""
     if out.dtype is not torch.bfloat16 or out.shape != (rows, cols) or out.device != dev or \
             (rows and cols and (out.stride(1) != 1 and cols > 1 or out.stride(0) < cols and rows > 1)):
         raise ValueError(f"out must be a bf16 tensor of shape {(rows, cols)} on {dev} with contiguous rows")
@@ -730,7 +732,7 @@ def int8_scaled_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, b_q: torch.Tensor
     _expect(a_scale, (M,), torch.float32, dev, "a_scale")
     _expect(b_scale, (N,), torch.float32, dev, "b_scale")
     cols = N // 2 if swiglu else N
-    out = _rows_out(out, M, cols, dev)
+    out = a_q.new_empty((M, cols), dtype=torch.bfloat16) if out is None else _rows_out(out, M, cols, dev)
     _checked(dev, "int8_scaled_gemm", a_q.data_ptr(), a_scale.data_ptr(), b_q.data_ptr(), b_scale.data_ptr(), M, N, K,
              1 if swiglu else 0, out.data_ptr(), out.stride(0) if M > 1 else max(cols, 1))
     return out
@@ -751,10 +753,15 @@ def int8_grouped_gemm(a_q: torch.Tensor, a_scale: torch.Tensor, offsets: torch.T
     _expect(a_scale, (rows,), torch.float32, dev, "a_scale")
     _expect(b_scale, (G, N), torch.float32, dev, "b_scale")
     cols = N // 2 if swiglu else N
-    out = _rows_out(out, rows, cols, dev)
+    out = a_q.new_empty((rows, cols), dtype=torch.bfloat16) if out is None else _rows_out(out, rows, cols, dev)
     _checked(dev, "int8_grouped_gemm", a_q.data_ptr(), a_scale.data_ptr(), offsets.data_ptr(), G, rows, b_q.data_ptr(),
              b_scale.data_ptr(), N, K, 1 if swiglu else 0, out.data_ptr(), out.stride(0) if rows > 1 else max(cols, 1))
     return out
+
+
+@functools.lru_cache(maxsize=None)
+def _qk_workspace(head_dim: int) -> int:
+    return workspace_bytes("qk_norm_backward", head_dim)
 
 
 class QKNormGrads(NamedTuple):
@@ -811,15 +818,16 @@ def qk_norm_rope(qkv: torch.Tensor, heads_q: int, heads_k: int, head_dim: int, p
     _expect_rows(qkv, tokens, width, dev, "qkv")
     axes, rot, pair_axis = _expect_rotation(tokens, positions, inv_freq, pair_axis, gamma_q, gamma_k, head_dim, dev)
     if out is None:
-        q = torch.empty((tokens, heads_q, head_dim), dtype=torch.bfloat16, device=dev)
-        k = torch.empty((tokens, heads_k, head_dim), dtype=torch.bfloat16, device=dev)
+        q, k = qkv.new_empty((tokens, heads_q, head_dim)), qkv.new_empty((tokens, heads_k, head_dim))
     else:
         q, k = out
         _expect_heads(q, tokens, heads_q, head_dim, dev, "out[0]")
         _expect_heads(k, tokens, heads_k, head_dim, dev, "out[1]")
+    qt, qh, _ = q.stride()
+    kt, kh, _ = k.stride()
     _checked(dev, "qk_norm_rope", qkv.data_ptr(), qkv.stride(0), tokens, heads_q, heads_k, head_dim, _at(gamma_q),
              _at(gamma_k), eps, positions.data_ptr(), axes, inv_freq.data_ptr(), rot, pair_axis, 1 if interleaved else 0,
-             q.data_ptr(), q.stride(0), q.stride(1), k.data_ptr(), k.stride(0), k.stride(1))
+             q.data_ptr(), qt, qh, k.data_ptr(), kt, kh)
     return q, k
 
 
@@ -848,7 +856,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: Optional[torc
         _expect_rows(qkv, tokens, width, dev, "qkv")
         ld = qkv.stride(0)
     if out is None:
-        out = torch.empty((tokens, width), dtype=torch.bfloat16, device=dev)
+        out = dq.new_empty((tokens, width))
     else:
         _expect_rows(out, tokens, width, dev, "out")
     gq = gk = None
@@ -857,12 +865,12 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: Optional[torc
         _expect(gq, (head_dim,), torch.float32, dev, "accumulate[0]")
         _expect(gk, (head_dim,), torch.float32, dev, "accumulate[1]")
     elif gamma_q is not None and want_dgamma:
-        gq = torch.empty(head_dim, dtype=torch.float32, device=dev)
-        gk = torch.empty(head_dim, dtype=torch.float32, device=dev)
+        gq, gk = gamma_q.new_empty(head_dim), gamma_q.new_empty(head_dim)
     if gq is not None and workspace is None:
-        workspace = torch.empty(workspace_bytes("qk_norm_backward", head_dim), dtype=torch.uint8, device=dev)
-    _checked(dev, "qk_norm_rope_backward", dq.data_ptr(), dq.stride(0), dq.stride(1), dk.data_ptr(), dk.stride(0),
-             dk.stride(1), _at(qkv), ld, tokens, heads_q, heads_k, head_dim, _at(gamma_q), _at(gamma_k), eps,
+        workspace = gamma_q.new_empty(_qk_workspace(head_dim) // 4)
+    qt, qh, _ = dq.stride()
+    kt, kh, _ = dk.stride()
+    _checked(dev, "qk_norm_rope_backward", dq.data_ptr(), qt, qh, dk.data_ptr(), kt, kh, _at(qkv), ld, tokens, heads_q, heads_k, head_dim, _at(gamma_q), _at(gamma_k), eps,
              positions.data_ptr(), axes, inv_freq.data_ptr(), rot, pair_axis, 1 if interleaved else 0, out.data_ptr(),
              out.stride(0), _at(gq), _at(gk), 1 if accumulate is not None else 0, _at(workspace),
              0 if workspace is None else _scratch(workspace, dev))

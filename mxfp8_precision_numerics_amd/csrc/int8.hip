@@ -581,7 +581,7 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
                     F[P ^ 1][2 * q + 1] = frag(a, b, P ^ 1, 2 * q + 1);
                 }
             }
-            if (q & 1) copy(q >> 1);
+            if (!(q & 1)) copy(q >> 1);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
