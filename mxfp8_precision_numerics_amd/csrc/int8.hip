@@ -482,6 +482,8 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // pair of A must have landed: B has one to two trips to arrive, A three to four.
 constexpr int LT = 256, LK = 64, LPAIR = 2 * LK, LREGION = LT * LPAIR, LREGIONS_A = 3;
 
+typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+
 // acc += b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the instruction
 // another destination and copies results about in the loop. The operands' loads are waited for by the compiler; nothing
 // else may write an operand or read a sum within 19 wait states (the kernel has 64 instructions between two uses of a
@@ -506,24 +508,36 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     const int64_t n_end = n0 + TC < cols ? n0 + TC : cols;
 
     // ------------------------------------------------------------------ scales of the wave's rows and columns
-    // Read here, ahead of the copies, so that the epilogue begins with them in registers.
+    // Read here, ahead of the copies, so that the epilogue begins with them in registers. A whole tile's come by addresses that
+    // differ by constants; an address, a clamp and a check for each cost more than the arithmetic on the sums (a wave is alone
+    // on its SIMD here, four cycles an instruction).
     const int r16 = lane & 15, q16 = lane >> 4;
     constexpr int NB = SWIGLU ? 4 : 8;                          // 16-column output blocks of a wave
-    const float* sb = g.sb + grp * g.N;
-    float sa[8], s_gate[NB][4], s_up[SWIGLU ? NB : 1][4];
+    const float* sb = g.sb + grp * g.N + n0 + wn * (TC / 2);
+    const float* sm = g.sa + m0 + wm * 128 + r16;
+    const bool whole = m_end - m0 == LT && n_end - n0 == TC;
+    float sa[8];
+    f32x4a s_gate[NB], s_up[SWIGLU ? NB : 1];
+    if (whole) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int64_t m = m0 + wm * 128 + j * 16 + r16;
-        sa[j] = g.sa[m < m_end ? m : m_end - 1];
-    }
+        for (int j = 0; j < 8; ++j) sa[j] = sm[16 * j];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int64_t n = n0 + wn * (TC / 2) + 16 * b + 4 * q16 + e, nc = n < cols ? n : cols - 1;
-            s_gate[b][e] = sb[nc];
-            if constexpr (SWIGLU) s_up[b][e] = sb[cols + nc];
+        for (int b = 0; b < NB; ++b) {
+            s_gate[b] = *reinterpret_cast<const f32x4a*>(sb + 4 * q16 + 16 * b);
+            if constexpr (SWIGLU) s_up[b] = *reinterpret_cast<const f32x4a*>(sb + cols + 4 * q16 + 16 * b);
         }
+    } else {
+        const int rows_left = (int)(m_end - 1 - m0) - wm * 128 - r16, cols_left = (int)(n_end - 1 - n0) - wn * (TC / 2);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sa[j] = sm[min(16 * j, rows_left)];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s_gate[b][e] = sb[min(16 * b + 4 * q16 + e, cols_left)];
+                if constexpr (SWIGLU) s_up[b][e] = sb[cols + min(16 * b + 4 * q16 + e, cols_left)];
+            }
+    }
 
     // ------------------------------------------------------------------ copies
     // Copy c (0 .. 7) of a wave fills rows 32c + 8 wave .. + 7 of a region: lane l brings row l / 8 of them, the chunk that
@@ -674,42 +688,52 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     // 16-lane row (v_permlane16_swap), which leaves a lane with 8 consecutive columns of one of them: lanes of row R hold
     // columns 16 (R % 2) + 8 (R / 2) .. of the pair's 32, and a 16-byte store writes 64 contiguous bytes into each of 16
     // rows.
-    const bool vec_ok = (g.ldc & 7) == 0 && (reinterpret_cast<uintptr_t>(g.c) & 15) == 0;
+    // output columns 32p .. of the wave, row block j: 8 consecutive ones of its row for each lane
+    auto outputs = [&](int p, int j) {
+        uint32_t w[2][2];
 #pragma unroll
-    for (int p = 0; p < NB / 2; ++p) {
-        const int64_t n = n0 + wn * (TC / 2) + p * 32 + 16 * (q16 & 1) + 8 * (q16 >> 1);
+        for (int h = 0; h < 2; ++h) {
+            const int b = 2 * p + h;
+            float v[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            uint32_t w[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int b = 2 * p + h;
-                float v[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (SWIGLU)
-                        v[e] = silu_times(int8_value(acc[2 * b][j][e], sa[j], s_gate[b][e]),
-                                          int8_value(acc[2 * b + 1][j][e], sa[j], s_up[b][e]));
-                    else
-                        v[e] = int8_value(acc[b][j][e], sa[j], s_gate[b][e]);
-                }
-                w[h][0] = pack_bf16(v[0], v[1]);
-                w[h][1] = pack_bf16(v[2], v[3]);
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (SWIGLU)
+                    v[e] = silu_times(int8_value(acc[2 * b][j][e], sa[j], s_gate[b][e]),
+                                      int8_value(acc[2 * b + 1][j][e], sa[j], s_up[b][e]));
+                else
+                    v[e] = int8_value(acc[b][j][e], sa[j], s_gate[b][e]);
             }
-            const auto x = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
-            const auto y = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
-            const int64_t m = m0 + wm * 128 + j * 16 + r16;
-            if (m >= m_end) continue;
-            uint16_t* dst = g.c + m * g.ldc + n;
-            const uint32_t d[4] = {(uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]};
-            if (vec_ok && n + 8 <= n_end) {
-                *reinterpret_cast<uint4*>(dst) = make_uint4(d[0], d[1], d[2], d[3]);
-            } else {
+            w[h][0] = pack_bf16(v[0], v[1]);
+            w[h][1] = pack_bf16(v[2], v[3]);
+        }
+        const auto x = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
+        const auto y = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
+        return make_uint4((uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]);
+    };
+    const bool vec_ok = (g.ldc & 7) == 0 && (reinterpret_cast<uintptr_t>(g.c) & 15) == 0;
+    const int row0 = wm * 128 + r16, col0 = wn * (TC / 2) + 16 * (q16 & 1) + 8 * (q16 >> 1);    // of the lane, within the tile
+    uint16_t* dst = g.c + (m0 + row0) * g.ldc + n0 + col0;
+    const bool plain = whole && vec_ok;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (n + e < n_end) dst[e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int p = 0; p < NB / 2; ++p) {
+            const uint4 d = outputs(p, j);
+            if (plain) {
+                *reinterpret_cast<uint4*>(dst + 32 * p) = d;
+            } else if (row0 + 16 * j < (int)(m_end - m0)) {
+                const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+                const int left = (int)(n_end - n0) - col0 - 32 * p;                  // columns from this lane's first on
+                if (vec_ok && left >= 8) {
+                    *reinterpret_cast<uint4*>(dst + 32 * p) = d;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < left) dst[32 * p + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                }
             }
         }
+        dst += 16 * g.ldc;
     }
 }
 
