@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
 }
 
 // W waves per row, NCH chunks of 8 values per lane, the row held in registers between the maximum and the codes (NCH = 0:
-// a row of any length, read twice). Bound by memory: 3 bytes a value.
+// a row of any length, read twice). Bound by memory, 3 bytes a value: 16384 x 8192 60.6 us, 6.6 TB/s.
 template <int W, int NCH>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void int8_quantize_kernel(const uint16_t* __restrict__ x,
                                                                             int64_t rows, int64_t cols,
@@ -480,6 +480,9 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // lies behind its first trip, where every wave has read the whole pair p: trip 2p + 1 then copies B's pair p + 2 into B's
 // region of p, trip 2p + 2 A's pair p + 3 into A's region of p. At the next barrier, behind trip 2p + 2, all but that last
 // pair of A must have landed: B has one to two trips to arrive, A three to four.
+// Measured: 4096 x 36864 x 12288 1.26 ms, 2.94 POP/s with the matrix unit busy 0.77 of the time; 131072 rows of 64 experts,
+// K = 2048 to 2 x 1024 with SwiGLU 531 us (2.07 POP/s), K = 1024 to 2048 364 us (1.51 POP/s): what a tile costs outside its
+// trips, about 9 us, weighs more the shorter its contraction.
 constexpr int LT = 256, LK = 64, LPAIR = 2 * LK, LREGION = LT * LPAIR, LREGIONS_A = 3;
 
 typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
@@ -743,7 +746,8 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
 // runs on its own: a ring of DEPTH such steps in LDS, filled past the registers by copies of whole lines (8 rows of 128 bytes
 // an instruction; loads of 16 rows of 64 bytes, as the matrix instruction wants them, read at 3.5 to 4.8 TB/s where these
 // read at 5.7 to 6.5), rows of 128 bytes swizzled as in the large tiles. The waves' sums meet in LDS by integer additions,
-// whose order does not matter.
+// whose order does not matter. Measured: 1 x 6144 x 2048 5.2 us; 16 tokens through 8 of 64 experts each, K = 2048 to 2 x 1024
+// with SwiGLU, 43.6 us (the chosen experts' weights at 5.4 TB/s).
 constexpr int FEW_W = 4;
 template <int MT, int NT, int DEPTH, bool GROUPED, bool SWIGLU>
 __global__ __launch_bounds__(64 * FEW_W) void int8_few_kernel(Int8Gemm g) {
