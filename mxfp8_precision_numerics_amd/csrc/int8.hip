@@ -5,6 +5,7 @@
 //   product:   C[m][n] = bf16( (sum_k a[m][k] b[n][k]) sa[m] sb[n] ),  the sum exact in 32-bit integers
 //   SwiGLU:    B holds F gate rows, then F up rows:  C[m][f] = bf16( silu(G[m][f]) U[m][f] ) from the products in fp32
 #pragma clang fp contract(off)
+#include <algorithm>
 #include <type_traits>
 
 #include "gemm_tile.h"
@@ -168,6 +169,7 @@ struct Int8Tile {
 };
 constexpr int GROUP_M = 4;              // row tiles that an XCD's workgroups walk together
 constexpr int64_t XCD_CHUNK = 32;       // consecutive tiles that an XCD takes at a time (grouped)
+constexpr int CUS = 256;                // of the chip
 
 template <int TM, bool GROUPED>
 __device__ __forceinline__ Int8Tile tile_of(const Int8Gemm& g, int tiles_n) {
@@ -202,9 +204,10 @@ __device__ __forceinline__ int first_step(uint32_t tile, int n) {
     return __builtin_amdgcn_readfirstlane((int)(((uint64_t)(tile * 0x9E3779B9u) * (uint32_t)n) >> 32));
 }
 
-// Resource of an operand's rows from `p` on, `rows` of them to the operand's end: what lies behind reads as zeros.
+// Resource of an operand's rows from `p` on, `rows` of them to the operand's end (a tile takes at most 256, and K is below
+// 2^17): what lies behind reads as zeros.
 __device__ __forceinline__ v4i rows_rsrc(const int8_t* p, int64_t rows, int64_t K) {
-    return buffer_rsrc(p, (uint32_t)(rows * K < 0x7FFFFFFF ? rows * K : 0x7FFFFFFF));
+    return buffer_rsrc(p, (uint32_t)(rows < 256 ? rows : 256) * (uint32_t)K);
 }
 
 // Middle tiles: 64 rows of A by 128 rows of B per workgroup; 4 waves side by side, each 64 x 32, as 16 x 16 accumulators of
@@ -466,8 +469,8 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 }
 
 // ---------------------------------------------------------------------------------------------------------------
-// Large tiles: 256 x 256 rows of A and B per workgroup, one workgroup per CU; 4 waves, 2 x 2, each 128 x 128 as 8 x 8
-// accumulators of 16 x 16 (256 registers). K advances 64 bytes per stage: one v_mfma_i32_16x16x64_i8 per accumulator.
+// Large tiles: 256 x 256 rows of A and B, one workgroup per CU, which takes its tiles in turn (LargeTiles); 4 waves, 2 x 2, each
+// 128 x 128 as 8 x 8 accumulators of 16 x 16 (256 registers). K advances 64 bytes per stage: one v_mfma_i32_16x16x64_i8 per accumulator.
 // (The chip is held back by its power here: from registers alone, on normally distributed codes, this instruction runs
 // at 4.2 POP/s and the 32 x 32 x 32 form at 3.4; on zeros both reach 4.9.) Operand of lane l: row l % 16, bytes 16 (l / 16)
 // .. + 15; B is the first operand, so register e of lane l holds output row l % 16, column 4 (l / 16) + e.
@@ -480,14 +483,23 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // lies behind its first trip, where every wave has read the whole pair p: trip 2p + 1 then copies B's pair p + 2 into B's
 // region of p, trip 2p + 2 A's pair p + 3 into A's region of p. At the next barrier, behind trip 2p + 2, all but that last
 // pair of A must have landed: B has one to two trips to arrive, A three to four.
-// Measured: 4096 x 36864 x 12288 1.26 ms, 2.94 POP/s with the matrix unit busy 0.77 of the time; 131072 rows of 64 experts,
-// K = 2048 to 2 x 1024 with SwiGLU 531 us (2.07 POP/s), K = 1024 to 2048 364 us (1.51 POP/s): what a tile costs outside its
-// trips, about 9 us, weighs more the shorter its contraction.
-constexpr int LT = 256, LK = 64, LPAIR = 2 * LK, LREGION = LT * LPAIR, LREGIONS_A = 3;
+// The pairs of a workgroup's tiles are one sequence: while a tile's last pairs are multiplied the next tile's first are copied, and
+// they land while its outputs are computed and stored. (With a workgroup for each tile, the search for the tile, the first pairs and
+// the scales took 11,000 of 44,000 cycles at K = 1024, where the trips take 23,000.)
+// Measured: 4096 x 36864 x 12288 1.20 ms, 3.09 POP/s; 131072 rows of 64 experts, K = 2048 to 2 x 1024 with SwiGLU 473 us
+// (2.32 POP/s; 522 with a workgroup for each tile), K = 1024 to 2048 307 us (1.79 POP/s; 357). What is left of a tile beside its
+// trips is mostly the arithmetic on the sums, 8,000 cycles (with SwiGLU 10,000), for which the matrix unit waits.
+constexpr int LT = 256, LPAIR = 128, LREGION = LT * LPAIR, LREGIONS_A = 3;
 
 typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// acc += b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the instruction
+// The same kind of resource as buffer_rsrc's, for loads and stores that the compiler issues and waits for.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int records) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, records, 0x00020000);
+}
+
+// acc += b a, and acc = b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the instruction
 // another destination and copies results about in the loop. The operands' loads are waited for by the compiler; nothing
 // else may write an operand or read a sum within 19 wait states (the kernel has 64 instructions between two uses of a
 // sum, and waits of its own around the last stage).
@@ -495,7 +507,98 @@ __device__ __forceinline__ void mfma_in_place(v4i& acc, v4i b, v4i a) {
     asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(acc) : "v"(b), "v"(a));
 }
 
-template <bool GROUPED, bool SWIGLU>
+__device__ __forceinline__ void mfma_from_zero(v4i& acc, v4i b, v4i a) {
+    asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, 0" : "+a"(acc) : "v"(b), "v"(a));
+}
+
+// The tiles that one workgroup takes in turn: every gridDim.x-th of an order in which each XCD (every eighth workgroup) walks a
+// contiguous run, so that the workgroups of an XCD share rows and weights in its L2. Grouped: a wave holds the rows of 64 groups
+// and the number of row tiles before each, a group a lane, and the next tile costs no memory access until one lies behind those.
+template <bool GROUPED>
+struct LargeTiles {
+    const Int8Gemm& g;
+    const int tiles_n;
+    int tiles_m, T, b = blockIdx.x;
+    int64_t base = 0, lo = 0, hi = 0;   // lane l: rows of group base + l
+    int before = 0, excl = 0, total = 0;
+
+    __device__ __forceinline__ LargeTiles(const Int8Gemm& g_, int tn) : g(g_), tiles_n(tn) {
+        int64_t rows;
+        if constexpr (GROUPED) {
+            load();
+            rows = total;
+            if (g.G > 64) {
+                for (base = 64; base < g.G; base += 64) {
+                    load();
+                    rows += total;
+                }
+                base = 0;
+                load();
+            }
+        } else {
+            rows = (g.M + LT - 1) / LT;
+        }
+        tiles_m = (int)(rows < 0x7FFFFFFF / tiles_n ? rows : 0x7FFFFFFF / tiles_n);
+        T = tiles_m * tiles_n;
+    }
+    __device__ __forceinline__ void load() {
+        const int lane = threadIdx.x & 63;
+        const int64_t q = base + lane;
+        lo = hi = 0;
+        if (q < g.G) {
+            lo = g.offsets[q];
+            hi = g.offsets[q + 1];
+            lo = lo < 0 ? 0 : (lo > g.M ? g.M : lo);
+            hi = hi < lo ? lo : (hi > g.M ? g.M : hi);
+        }
+        const int nt = (int)((hi - lo + LT - 1) / LT);
+        int incl = nt;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int v = __shfl_up(incl, off, 64);
+            if (lane >= off) incl += v;
+        }
+        excl = incl - nt;
+        total = __builtin_amdgcn_readlane(incl, 63);
+    }
+    __device__ __forceinline__ static int64_t lane_value(int64_t v, int lane) {
+        return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)v, lane) |
+                         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32);
+    }
+    __device__ __forceinline__ Int8Tile next() {
+        Int8Tile r{0, 0, -1, 0};
+        if (b >= T) return r;
+        const int T8 = T & ~7, v = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
+        b += (int)gridDim.x;
+        if constexpr (GROUPED) {
+            const int row = v / tiles_n;
+            while (row - before >= total) {
+                if (base + 64 >= g.G) return r;
+                base += 64;
+                before += total;
+                load();
+            }
+            const int at = row - before;
+            const int L = 63 - __builtin_clzll(__ballot(excl <= at));     // the last group with that many tiles before it
+            r.grp = base + L;
+            r.m0 = lane_value(lo, L) + (int64_t)(at - __builtin_amdgcn_readlane(excl, L)) * LT;
+            const int64_t end = lane_value(hi, L);
+            r.m_end = r.m0 + LT < end ? r.m0 + LT : end;
+            r.n = v - row * tiles_n;
+        } else {
+            // in groups of GROUP_M row tiles
+            const int per_group = GROUP_M * tiles_n, first_m = (v / per_group) * GROUP_M;
+            const int gm = min(GROUP_M, tiles_m - first_m), x = v % per_group;
+            r.grp = 0;
+            r.m0 = (int64_t)(first_m + x % gm) * LT;
+            r.n = x / gm;
+            r.m_end = r.m0 + LT < g.M ? r.m0 + LT : g.M;
+        }
+        return r;
+    }
+};
+
+template <bool GROUPED, bool SWIGLU, bool ALIGNED>
 __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[(LREGIONS_A + 2) * LREGION];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -503,61 +606,54 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     const int wm = wave & 1, wn = wave >> 1;
     const int64_t cols = SWIGLU ? g.N / 2 : g.N;
     constexpr int TC = SWIGLU ? LT / 2 : LT;
-    const Int8Tile tile = tile_of<LT, GROUPED>(g, (int)((cols + TC - 1) / TC));
+    LargeTiles<GROUPED> tiles(g, (int)((cols + TC - 1) / TC));
+    Int8Tile tile = tiles.next();
     if (tile.grp < 0) return;
-    const int64_t m0 = tile.m0, m_end = tile.m_end, n0 = tile.n * TC, grp = tile.grp;
-    const int8_t* A = g.a + m0 * g.K;
-    const int8_t* B = g.b + (grp * g.N + n0) * g.K;             // SwiGLU: the gate rows; the up rows are cols rows further
-    const int64_t n_end = n0 + TC < cols ? n0 + TC : cols;
-
-    // ------------------------------------------------------------------ scales of the wave's rows and columns
-    // Read here, ahead of the copies, so that the epilogue begins with them in registers. A whole tile's come by addresses that
-    // differ by constants; an address, a clamp and a check for each cost more than the arithmetic on the sums (a wave is alone
-    // on its SIMD here, four cycles an instruction).
     const int r16 = lane & 15, q16 = lane >> 4;
-    constexpr int NB = SWIGLU ? 4 : 8;                          // 16-column output blocks of a wave
-    const float* sb = g.sb + grp * g.N + n0 + wn * (TC / 2);
-    const float* sm = g.sa + m0 + wm * 128 + r16;
-    const bool whole = m_end - m0 == LT && n_end - n0 == TC;
-    float sa[8];
-    f32x4a s_gate[NB], s_up[SWIGLU ? NB : 1];
-    if (whole) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sa[j] = sm[16 * j];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            s_gate[b] = *reinterpret_cast<const f32x4a*>(sb + 4 * q16 + 16 * b);
-            if constexpr (SWIGLU) s_up[b] = *reinterpret_cast<const f32x4a*>(sb + cols + 4 * q16 + 16 * b);
-        }
-    } else {
-        const int rows_left = (int)(m_end - 1 - m0) - wm * 128 - r16, cols_left = (int)(n_end - 1 - n0) - wn * (TC / 2);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sa[j] = sm[min(16 * j, rows_left)];
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s_gate[b][e] = sb[min(16 * b + 4 * q16 + e, cols_left)];
-                if constexpr (SWIGLU) s_up[b][e] = sb[cols + min(16 * b + 4 * q16 + e, cols_left)];
-            }
-    }
 
     // ------------------------------------------------------------------ copies
     // Copy c (0 .. 7) of a wave fills rows 32c + 8 wave .. + 7 of a region: lane l brings row l / 8 of them, the chunk that
     // belongs at position l % 8. The resources end with the operand: rows behind its end are zeros, rows of A behind the
-    // group's are the next group's, and what a last pair asks for past the end of K is a part of the next row (their
-    // outputs are never stored, and the last is masked).
-    const v4i rA = rows_rsrc(A, g.M - m0, g.K);
-    const v4i rB = rows_rsrc(SWIGLU && wave >= 2 ? B + cols * g.K : B, cols - n0, g.K);        // waves 2, 3 bring up rows
+    // group's are the next group's (their outputs are never stored).
+    auto a_rows = [&](const Int8Tile& t) {
+        return t.grp < 0 ? buffer_rsrc(g.a, 0) : rows_rsrc(g.a + t.m0 * g.K, g.M - t.m0, g.K);
+    };
+    auto b_rows = [&](const Int8Tile& t) {                      // SwiGLU: waves 0, 1 bring gate rows, waves 2, 3 up rows
+        const int64_t n0 = t.n * TC;
+        return t.grp < 0 ? buffer_rsrc(g.b, 0) : rows_rsrc(g.b + (t.grp * g.N + n0 + (SWIGLU && wave >= 2 ? cols : 0)) * g.K, cols - n0, g.K);
+    };
     const int brow = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
     const int K = (int)g.K;
     const int a_off = brow * K + 16 * chunk, b_off = (SWIGLU ? brow & 15 : brow) * K + 16 * chunk;
     const int a_step = 32 * K, b_step = SWIGLU ? 16 * K : 32 * K;
     const uint32_t lds0 = lds_offset(&lds[1024 * wave]);
-    // copy c of pair p into the region at byte `into`
-    auto copy_a = [&](int p, uint32_t into, int c) { dma_to_lds<16>(rA, lds0 + into + 4096 * c, a_off + c * a_step, p * LPAIR); };
-    auto copy_b = [&](int p, uint32_t into, int c) { dma_to_lds<16>(rB, lds0 + into + 4096 * c, b_off + c * b_step, p * LPAIR); };
     constexpr uint32_t B0 = LREGIONS_A * LREGION;               // B's regions
+    // Pairs of a tile: at least three, so that copies reach no further ahead than the next tile; a shorter contraction is filled up
+    // with pairs whose A is zeros. What the last pair holds past the end of K is zeros in A too (an offset out of range).
+    const int pairs = (K + LPAIR - 1) / LPAIR, np = max(pairs, 3), fill = np - pairs;
+    const int a_none = 0x7F000000, a_last = 16 * chunk < K - LPAIR * (pairs - 1) ? a_off : a_none, a_first = pairs == 1 ? a_last : a_off;
+    // The pairs of one operand in the order they are copied: a tile's, then the next tile's. Behind the last tile an empty operand.
+    struct Stream {
+        v4i rows;
+        int k, step, left, off;                                 // byte of K, what a pair advances it by, pairs left of the tile
+    };
+    Stream in_a{a_rows(tile), 0, LPAIR, np, a_first}, in_b{b_rows(tile), 0, LPAIR, np, b_off};
+    v4i next_a = in_a.rows, next_b = in_b.rows;
+    int next_step = 0;
+    auto turn = [&](Stream& s, const v4i& next, int off) {      // before a pair's copies
+        if (s.left == 0) s = Stream{next, 0, next_step, np, off};
+    };
+    auto done = [&](Stream& s) {                                // behind them
+        s.k += s.step;
+        if (--s.left == fill) s.k = s.step = 0;                 // an offset of K past the operand's end would wrap around
+    };
+    auto aim_a = [&]() { in_a.off = in_a.left > fill + 1 ? a_off : in_a.left == fill + 1 ? a_last : a_none; };
+    auto done_a = [&]() {
+        done(in_a);
+        aim_a();
+    };
+    auto copy_a = [&](uint32_t into, int c) { dma_to_lds<16>(in_a.rows, lds0 + into + 4096 * c, in_a.off + c * a_step, in_a.k); };
+    auto copy_b = [&](uint32_t into, int c) { dma_to_lds<16>(in_b.rows, lds0 + into + 4096 * c, b_off + c * b_step, in_b.k); };
 
     // ------------------------------------------------------------------ fragments and matrix instructions
     const int in_row[2] = {r16 * LPAIR + 16 * (q16 ^ (r16 >> 1)), r16 * LPAIR + 16 * ((4 + q16) ^ (r16 >> 1))};
@@ -570,7 +666,7 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+        for (int j = 0; j < 8; ++j) asm volatile("" : "=a"(acc[i][j]));        // written by a tile's first trip
     // Everything that writes the sums before this statement has been issued, and nothing that reads them has.
     auto settle = [&]() {
 #pragma unroll
@@ -580,9 +676,10 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     };
     v4i F[2][16];                                               // two sets of fragments
 
-    // One trip in 16 steps of 4 instructions: set P is multiplied; with READ, half P ^ 1 of the pair in regions (a, b) is read
-    // into the other set, two fragments in each of the first 8 steps; a copy (copy(c), c = 0 .. 7) goes in every other step.
-    auto trip = [&](auto p_c, auto read_c, uint32_t a, uint32_t b, auto&& copy) {
+    // One trip in 16 steps of 4 instructions: set P is multiplied (a tile's first trip begins the sums); half P ^ 1 of the pair in
+    // regions (a, b) is read into the other set, two fragments in each of the first 8 steps; a copy (copy(c), c = 0 .. 7) goes in
+    // every other step.
+    auto trip = [&](auto p_c, auto first_c, uint32_t a, uint32_t b, auto&& copy) {
         constexpr int P = decltype(p_c)::value;
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
@@ -590,13 +687,12 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int j = 4 * (q & 1) + x;
-                mfma_in_place(acc[i][j], F[P][8 + i], F[P][j]);
+                if constexpr (decltype(first_c)::value) mfma_from_zero(acc[i][j], F[P][8 + i], F[P][j]);
+                else mfma_in_place(acc[i][j], F[P][8 + i], F[P][j]);
             }
-            if constexpr (decltype(read_c)::value) {
-                if (q < 8) {
-                    F[P ^ 1][2 * q] = frag(a, b, P ^ 1, 2 * q);
-                    F[P ^ 1][2 * q + 1] = frag(a, b, P ^ 1, 2 * q + 1);
-                }
+            if (q < 8) {
+                F[P ^ 1][2 * q] = frag(a, b, P ^ 1, 2 * q);
+                F[P ^ 1][2 * q + 1] = frag(a, b, P ^ 1, 2 * q + 1);
             }
             if (!(q & 1)) copy(q >> 1);
             __builtin_amdgcn_sched_barrier(0);
@@ -606,138 +702,166 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     using T1 = std::integral_constant<int, 1>;
     constexpr std::true_type yes{};
     constexpr std::false_type no{};
-    auto none = [](int) {};
-    // What a last pair holds past K becomes zero in A (selects: the sums keep one path).
-    const int rem = (int)(g.K % LPAIR);                         // 0, 32, 64 or 96
-    auto mask = [&](auto p_c) {
-        constexpr int P = decltype(p_c)::value;
-        const int keep = rem == 0 || 16 * (4 * P + q16) < rem ? -1 : 0;
-#pragma unroll
-        for (int f = 0; f < 8; ++f)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) F[P][f][e] &= keep;
-        // the selects' results to the matrix instructions
-        asm volatile("s_nop 7" : "+v"(F[P][0]), "+v"(F[P][1]), "+v"(F[P][2]), "+v"(F[P][3]), "+v"(F[P][4]), "+v"(F[P][5]),
-                                 "+v"(F[P][6]), "+v"(F[P][7]));
-    };
 
-    // ------------------------------------------------------------------ prologue: pairs 0 and 1, and A's pair 2
-    const int np = (int)((g.K + LPAIR - 1) / LPAIR);
+    // ------------------------------------------------------------------ prologue: the first tile's pairs 0 and 1
 #pragma unroll
-    for (int c = 0; c < 8; ++c) copy_a(0, 0, c);
+    for (int c = 0; c < 8; ++c) copy_a(0, c);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) copy_b(0, B0, c);
-    if (np > 1) {
+    for (int c = 0; c < 8; ++c) copy_b(B0, c);
+    done_a();
+    done(in_b);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) copy_a(1, LREGION, c);
+    for (int c = 0; c < 8; ++c) copy_a(LREGION, c);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) copy_b(1, B0 + LREGION, c);
-    }
-    if (np > 2) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) copy_a(2, 2 * LREGION, c);
-    }
-    settle();                                                   // the zeros are written while the first pairs are on their way
-    if (np > 2) wait_copies_barrier<24>();
-    else if (np > 1) wait_copies_barrier<16>();
-    else wait_copies_barrier<0>();
+    for (int c = 0; c < 8; ++c) copy_b(B0 + LREGION, c);
+    done_a();
+    done(in_b);
+    wait_copies_barrier<16>();
 #pragma unroll
     for (int f = 0; f < 16; ++f) F[0][f] = frag(0, B0, 0, f);
-    if (np == 1) mask(T0{});
-    trip(T0{}, yes, 0, B0, none);
-    if (np > 2) wait_copies_barrier<8>();
-    else wait_copies_barrier<0>();
-    __builtin_amdgcn_s_waitcnt(0xC07F);                         // the compiler's own view of that wait
 
-    // ------------------------------------------------------------------ pairs
-    int p = 0;
-    uint32_t a0 = 0, a1 = LREGION, b0 = B0, b1 = B0 + LREGION;  // regions of pairs p and p + 1
+    uint32_t a0 = 2 * LREGION, a1 = 0, b0 = B0 + LREGION, b1 = B0;      // regions of the pair before and the next one
     auto next = [&]() {
         a0 = a1;
         a1 = a1 == 2 * LREGION ? 0u : a1 + LREGION;
         const uint32_t x = b0;
         b0 = b1;
         b1 = x;
-        ++p;
     };
-    while (p + 3 < np) {
-        trip(T1{}, yes, a1, b1, [&](int c) { copy_b(p + 2, b0, c); });
-        trip(T0{}, yes, a1, b1, [&](int c) { copy_a(p + 3, a0, c); });
+    auto pair_end = [&]() {
         wait_copies_barrier<8>();
-        __builtin_amdgcn_s_waitcnt(0xC07F);
+        __builtin_amdgcn_s_waitcnt(0xC07F);                     // the compiler's own view of that wait
         next();
-    }
-    while (p + 1 < np) {                                        // at most B's pair p + 2 is still to be copied
-        if (p + 2 < np) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) copy_b(p + 2, b0, c);
-        }
-        trip(T1{}, yes, a1, b1, none);
-        if (p + 2 == np && rem) mask(T0{});
-        trip(T0{}, yes, a1, b1, none);
-        wait_copies_barrier<0>();
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        next();
-    }
-    if (rem == 0 || rem > LK) {                                 // the last half, if K reaches into it
-        if (rem) mask(T1{});
-        trip(T1{}, no, 0, 0, none);
-    }
-    asm volatile("s_nop 15\n\ts_nop 15");                       // the matrix instructions' results to what reads them
-    settle();
-
-    // ------------------------------------------------------------------ epilogue
-    // Lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block. Two blocks side by side swap every other
-    // 16-lane row (v_permlane16_swap), which leaves a lane with 8 consecutive columns of one of them: lanes of row R hold
-    // columns 16 (R % 2) + 8 (R / 2) .. of the pair's 32, and a 16-byte store writes 64 contiguous bytes into each of 16
-    // rows.
-    // output columns 32p .. of the wave, row block j: 8 consecutive ones of its row for each lane
-    auto outputs = [&](int p, int j) {
-        uint32_t w[2][2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int b = 2 * p + h;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (SWIGLU)
-                    v[e] = silu_times(int8_value(acc[2 * b][j][e], sa[j], s_gate[b][e]),
-                                      int8_value(acc[2 * b + 1][j][e], sa[j], s_up[b][e]));
-                else
-                    v[e] = int8_value(acc[b][j][e], sa[j], s_gate[b][e]);
-            }
-            w[h][0] = pack_bf16(v[0], v[1]);
-            w[h][1] = pack_bf16(v[2], v[3]);
-        }
-        const auto x = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
-        const auto y = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
-        return make_uint4((uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]);
     };
-    const bool vec_ok = (g.ldc & 7) == 0 && (reinterpret_cast<uintptr_t>(g.c) & 15) == 0;
-    const int row0 = wm * 128 + r16, col0 = wn * (TC / 2) + 16 * (q16 & 1) + 8 * (q16 >> 1);    // of the lane, within the tile
-    uint16_t* dst = g.c + (m0 + row0) * g.ldc + n0 + col0;
-    const bool plain = whole && vec_ok;
+    const int inner = max(np - 4, 0);                           // iterations whose copies are neither a tile's first nor its last pair
+    for (;;) {
+        trip(T0{}, yes, a1, b1, [&](int c) { copy_a(a0, c); });
+        done_a();
+        pair_end();
+        const Int8Tile after = tiles.next();
+        next_a = a_rows(after);
+        next_b = b_rows(after);
+        next_step = after.grp < 0 ? 0 : LPAIR;
+        int p = 0;
+        for (; p < inner; ++p) {                                // pairs p + 2 of B, p + 3 of A
+            trip(T1{}, no, a1, b1, [&](int c) { copy_b(b0, c); });
+            in_b.k += LPAIR;
+            trip(T0{}, no, a1, b1, [&](int c) { copy_a(a0, c); });
+            in_a.k += LPAIR;
+            pair_end();
+        }
+        in_b.left -= inner;
+        in_a.left -= inner;
+        aim_a();
+        for (; p + 1 < np; ++p) {
+            turn(in_b, next_b, b_off);
+            trip(T1{}, no, a1, b1, [&](int c) { copy_b(b0, c); });
+            done(in_b);
+            turn(in_a, next_a, a_first);
+            trip(T0{}, no, a1, b1, [&](int c) { copy_a(a0, c); });
+            done_a();
+            pair_end();
+        }
+
+        // -------------------------------------------------------------- scales of the wave's rows and columns
+        // Read ahead of the last trip. A whole tile's come by addresses that differ by constants; an address, a clamp and a check
+        // for each cost more than the arithmetic on the sums (a wave is alone on its SIMD here, four cycles an instruction).
+        const int64_t m0 = tile.m0, m_end = tile.m_end, n0 = tile.n * TC, grp = tile.grp;
+        const int64_t n_end = n0 + TC < cols ? n0 + TC : cols;
+        constexpr int NB = SWIGLU ? 4 : 8;                          // 16-column output blocks of a wave
+        const float* sb = g.sb + grp * g.N + n0 + wn * (TC / 2);
+        const float* sm = g.sa + m0 + wm * 128;
+        float sa[8];
+        f32x4a s_gate[NB], s_up[SWIGLU ? NB : 1];
+        const int rows_left = (int)(m_end - m0) - wm * 128, cols_left = (int)(n_end - n0) - wn * (TC / 2);    // of the wave
+        if constexpr (ALIGNED) {
+            // bytes behind a tile's last row or column are out of the buffer's range and read as zeros
+            const auto ra = buffer_of(sm, 4 * max(rows_left, 0)), rg = buffer_of(sb, 4 * max(cols_left, 0));
+            const auto ru = buffer_of(sb + cols, SWIGLU ? 4 * max(cols_left, 0) : 0);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < 8; ++j) sa[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ra, 4 * r16 + 64 * j, 0, 0));
 #pragma unroll
-        for (int p = 0; p < NB / 2; ++p) {
-            const uint4 d = outputs(p, j);
-            if (plain) {
-                *reinterpret_cast<uint4*>(dst + 32 * p) = d;
-            } else if (row0 + 16 * j < (int)(m_end - m0)) {
-                const uint32_t w[4] = {d.x, d.y, d.z, d.w};
-                const int left = (int)(n_end - n0) - col0 - 32 * p;                  // columns from this lane's first on
-                if (vec_ok && left >= 8) {
-                    *reinterpret_cast<uint4*>(dst + 32 * p) = d;
-                } else {
+            for (int b = 0; b < NB; ++b) {
+                s_gate[b] = __builtin_bit_cast(f32x4a, __builtin_amdgcn_raw_buffer_load_b128(rg, 16 * q16 + 64 * b, 0, 0));
+                if constexpr (SWIGLU)
+                    s_up[b] = __builtin_bit_cast(f32x4a, __builtin_amdgcn_raw_buffer_load_b128(ru, 16 * q16 + 64 * b, 0, 0));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sa[j] = sm[min(16 * j + r16, rows_left - 1)];
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s_gate[b][e] = sb[min(16 * b + 4 * q16 + e, cols_left - 1)];
+                    if constexpr (SWIGLU) s_up[b][e] = sb[cols + min(16 * b + 4 * q16 + e, cols_left - 1)];
+                }
+        }
+        turn(in_b, next_b, b_off);
+        trip(T1{}, no, a1, b1, [&](int c) { copy_b(b0, c); });
+        asm volatile("s_nop 15\n\ts_nop 15");                   // the matrix instructions' results to what reads them
+        settle();
+
+        // ------------------------------------------------------------------ epilogue
+        // Lane l holds columns 4 (l / 16) .. + 3 of row l % 16 of each 16 x 16 block. Two blocks side by side swap every other
+        // 16-lane row (v_permlane16_swap), which leaves a lane with 8 consecutive columns of one of them: lanes of row R hold
+        // columns 16 (R % 2) + 8 (R / 2) .. of the pair's 32, and a 16-byte store writes 64 contiguous bytes into each of 16
+        // rows.
+        // output columns 32p .. of the wave, row block j: 8 consecutive ones of its row for each lane
+        auto outputs = [&](int p, int j) {
+            uint32_t w[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int b = 2 * p + h;
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (SWIGLU)
+                        v[e] = silu_times(int8_value(acc[2 * b][j][e], sa[j], s_gate[b][e]),
+                                          int8_value(acc[2 * b + 1][j][e], sa[j], s_up[b][e]));
+                    else
+                        v[e] = int8_value(acc[b][j][e], sa[j], s_gate[b][e]);
+                }
+                w[h][0] = pack_bf16(v[0], v[1]);
+                w[h][1] = pack_bf16(v[2], v[3]);
+            }
+            const auto x = __builtin_amdgcn_permlane16_swap(w[0][0], w[1][0], false, false);
+            const auto y = __builtin_amdgcn_permlane16_swap(w[0][1], w[1][1], false, false);
+            return u32x4{(uint32_t)x[0], (uint32_t)y[0], (uint32_t)x[1], (uint32_t)y[1]};
+        };
+        const int col0 = 16 * (q16 & 1) + 8 * (q16 >> 1);                               // of the lane, within the wave's
+        uint16_t* dst = g.c + (m0 + wm * 128) * g.ldc + n0 + wn * (TC / 2);
+        if constexpr (ALIGNED) {
+            const uint32_t row_bytes = 2 * (uint32_t)g.ldc;
+            const auto rc = buffer_of(dst, (int)(max(rows_left, 0) * row_bytes));              // rows behind the last are left as they were
+            uint32_t at[NB / 2];
+#pragma unroll
+            for (int p = 0; p < NB / 2; ++p) at[p] = col0 + 32 * p < cols_left ? r16 * row_bytes + 2 * (col0 + 32 * p) : 0x7F000000u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int p = 0; p < NB / 2; ++p)
+                    __builtin_amdgcn_raw_buffer_store_b128(outputs(p, j), rc, (int)(at[p] + 16 * j * row_bytes), 0, 0);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint16_t* row = dst + (r16 + 16 * j) * g.ldc + col0;
+#pragma unroll
+                for (int p = 0; p < NB / 2; ++p) {
+                    const u32x4 d = outputs(p, j);
+                    const int left = r16 + 16 * j < rows_left ? cols_left - col0 - 32 * p : 0;   // columns from this lane's first on
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        if (e < left) dst[32 * p + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+                        if (e < left) row[32 * p + e] = (uint16_t)(d[e >> 1] >> (16 * (e & 1)));
                 }
             }
         }
-        dst += 16 * g.ldc;
+        done(in_b);
+        if (after.grp < 0) break;
+        tile = after;
+        settle();
     }
+    wait_copies_barrier<0>();                                   // no copy may arrive behind the workgroup's end
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -944,7 +1068,11 @@ template <bool GROUPED, bool SWIGLU>
 static void launch_products(const Int8Gemm& g, int64_t cols, hipStream_t stream) {
     const Int8Plan p = int8_plan(g.M, cols, g.K, g.G, SWIGLU);
     const dim3 blocks((unsigned)p.blocks), threads(256);
-    if (p.kind == INT8_LARGE) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
+    // 16-byte stores by 32-bit offsets within a tile
+    const bool aligned = cols % 8 == 0 && g.ldc % 8 == 0 && g.ldc < (1 << 21) && (reinterpret_cast<uintptr_t>(g.c) & 15) == 0;
+    const dim3 cus((unsigned)std::min<int64_t>(p.blocks, CUS));
+    if (p.kind == INT8_LARGE && aligned) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU, true>), cus, threads, 0, stream, g);
+    else if (p.kind == INT8_LARGE) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU, false>), cus, threads, 0, stream, g);
     else if (p.kind == INT8_MIDDLE && p.deep) hipLaunchKernelGGL((int8_gemm_kernel<3, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
     else if (p.kind == INT8_MIDDLE) hipLaunchKernelGGL((int8_gemm_kernel<2, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
     else if (p.kind == INT8_WIDE && p.wide <= 4) launch_wide<4, SWIGLU>(g, p, stream);

@@ -137,6 +137,51 @@ def test_dense(M, N, K, swiglu):
     _check(mxq.int8_scaled_gemm(a, sa, b, sb, swiglu=swiglu), _sums(a, b), sa, sb, swiglu)
 
 
+# Large tiles that workgroups take in turn, two to five each: the next tile's first pairs are copied while a tile still runs.
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K", [32, 96, 128, 160, 256, 288, 384, 416, 512, 640, 1024])
+@pytest.mark.parametrize("N", [16392, 16390])                             # 16-byte stores, and columns one by one
+def test_large_tiles_in_turn(N, K, swiglu):
+    M = 2100
+    g = _gen(N + K)
+    a, sa, b, sb = _operands(g, M, N, K)
+    if swiglu:
+        sa = sa * 0.001
+    cols = N // 2 if swiglu else N
+    wide = torch.full((M + 2, cols + (24 if N % 16 == 8 else 3)), 7.0, dtype=torch.bfloat16, device=DEV)
+    say("int8_scaled_gemm", M, N, K, swiglu)
+    c = mxq.int8_scaled_gemm(a, sa, b, sb, swiglu=swiglu, out=wide[1:-1, 8:8 + cols] if N % 16 == 8 else wide[1:-1, 3:])
+    s = _sums(a, b)
+    _check(c, s, sa, sb, swiglu)
+    left = 8 if N % 16 == 8 else 3
+    assert bool((wide[0] == 7.0).all()) and bool((wide[-1] == 7.0).all())
+    assert bool((wide[:, :left] == 7.0).all()) and bool((wide[:, left + cols:] == 7.0).all())
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("G,K", [(64, 96), (130, 288), (200, 544)])
+def test_large_grouped_tiles_in_turn(G, K, swiglu):
+    """Ragged experts, some empty and some of several tiles, more of them than a wave holds at once."""
+    N = 2064
+    g = _gen(G + K)
+    sizes = torch.randint(0, 260, (G,), generator=g, device=DEV)
+    sizes[3] = sizes[4] = sizes[-1] = 0
+    sizes[5], sizes[G // 2] = 700, 513
+    off = torch.cat([torch.tensor([5], device=DEV), 5 + torch.cumsum(sizes, 0)])
+    rows = int(off[-1]) + 300
+    a, sa, b, sb = _operands(g, rows, N, K, G)
+    if swiglu:
+        sa = sa * 0.001
+    out = torch.full((rows, N // 2 if swiglu else N), 7.0, dtype=torch.bfloat16, device=DEV)
+    say("int8_grouped_gemm", G, rows, N, K, swiglu)
+    c = mxq.int8_grouped_gemm(a, sa, off, b, sb, swiglu=swiglu, out=out)
+    o = off.tolist()
+    for e in range(G):
+        if o[e] < o[e + 1]:
+            _check(c[o[e]:o[e + 1]], _sums(a[o[e]:o[e + 1]], b[e]), sa[o[e]:o[e + 1]], sb[e], swiglu)
+    assert bool((c[:5] == 7.0).all()) and bool((c[o[-1]:] == 7.0).all())
+
+
 def test_largest_sums():
     """-128 times -128 over the longest contraction: the sum just fits 32 bits."""
     need_gpu()

@@ -55,7 +55,7 @@ def _states(insn):
 
 def test_large_tile_kernels(tmp_path):
     code = {n: c for n, c in _kernels(str(tmp_path)).items() if "int8_gemm_large_kernel" in n}
-    assert len(code) == 4
+    assert len(code) == 8
     for name, insns in code.items():
         assert not any(i.startswith("scratch_") for i in insns), name
         issued, written = {}, {}                     # register -> wait states since, in the order of the code
@@ -66,7 +66,7 @@ def test_large_tile_kernels(tmp_path):
             if op.startswith("v_mfma"):
                 count += 1
                 dst = _registers(operands[0])
-                assert operands[0] == operands[3], (name, insn)          # in place
+                assert operands[3] in (operands[0], "0"), (name, insn)   # in place, or a tile's first: from zero
                 for r in _registers(operands[1]) | _registers(operands[2]) | dst:
                     assert now - written.get(r, -99) > BEFORE, (name, insn)
                 for r in dst:
@@ -78,4 +78,4 @@ def test_large_tile_kernels(tmp_path):
                     for r in _registers(operands[0]):
                         written[r] = now
             now += _states(insn)
-        assert count > 300, name
+        assert count >= 256, name
