@@ -486,8 +486,8 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // The pairs of a workgroup's tiles are one sequence: while a tile's last pairs are multiplied the next tile's first are copied, and
 // they land while its outputs are computed and stored. (With a workgroup for each tile, the search for the tile, the first pairs and
 // the scales took 11,000 of 44,000 cycles at K = 1024, where the trips take 23,000.)
-// Measured: 4096 x 36864 x 12288 1.20 ms, 3.09 POP/s; 131072 rows of 64 experts, K = 2048 to 2 x 1024 with SwiGLU 473 us
-// (2.32 POP/s; 522 with a workgroup for each tile), K = 1024 to 2048 307 us (1.79 POP/s; 357). What is left of a tile beside its
+// Measured: 4096 x 36864 x 12288 1.20 to 1.23 ms, 3.0 POP/s (1.22 to 1.26 with a workgroup for each tile); 131072 rows of 64 experts,
+// K = 2048 to 2 x 1024 with SwiGLU 473 to 484 us, 2.3 POP/s (522), K = 1024 to 2048 307 to 313 us, 1.8 POP/s (357). What is left of a tile beside its
 // trips is mostly the arithmetic on the sums, 8,000 cycles (with SwiGLU 10,000), for which the matrix unit waits.
 constexpr int LT = 256, LPAIR = 128, LREGION = LT * LPAIR, LREGIONS_A = 3;
 
