@@ -500,7 +500,8 @@ mxq_status qk_norm_rope(const uint16_t* qkv_bf16, int64_t ld, int64_t tokens, in
  *   dqkv_bf16[tokens][ld_d], the heads laid out as in qkv_bf16: bf16_rne(rstd (t - xh (sum_d t xh) / head_dim)), or bf16_rne(d)
  *   without a norm; columns past the heads are left as they were (attention's backward writes the values' gradient there);
  *   dgamma_q, dgamma_k (fp32[head_dim], both or neither): sum over tokens and heads of d xh; accumulate != 0 adds it. The
- *   sums are formed in a fixed order.
+ *   sums are formed in a fixed order. They are written side by side: buffers that overlap are refused, also where both kinds
+ *   of heads share their gamma.
  * qkv_bf16 may be NULL without a norm (dgamma must then be NULL). dqkv_bf16 may be qkv_bf16 itself. workspace:
  * mxq_workspace_bytes("qk_norm_backward", head_dim) bytes, clobbered (needed only for dgamma). With no tokens dgamma is zeroed
  * (or left alone when accumulating). Requirements as for qk_norm_rope.

@@ -839,7 +839,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: Optional[torc
     """Gradients of qk_norm_rope: dq and dk bf16 [tokens][heads][head_dim] (views of any token and head strides), qkv its
     input (None without a norm). dqk is bf16 [tokens][(heads_q + heads_k) * head_dim]; `out` may hold wider rows, whose
     further columns are left as they were, or be qkv itself. dgamma_q and dgamma_k are new float32[head_dim], or are added
-    into the pair `accumulate`; None without a norm or with want_dgamma=False."""
+    into the pair `accumulate` (two buffers, also for a shared gamma); None without a norm or with want_dgamma=False."""
     if not dq.is_cuda or dq.dim() != 3 or dk.dim() != 3:
         raise ValueError("dq and dk must be device tensors [tokens][heads][head_dim]")
     tokens, heads_q, head_dim = dq.shape
@@ -870,8 +870,8 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: Optional[torc
         workspace = gamma_q.new_empty(_qk_workspace(head_dim) // 4)
     qt, qh, _ = dq.stride()
     kt, kh, _ = dk.stride()
-    _checked(dev, "qk_norm_rope_backward", dq.data_ptr(), qt, qh, dk.data_ptr(), kt, kh, _at(qkv), ld, tokens, heads_q, heads_k, head_dim, _at(gamma_q), _at(gamma_k), eps,
-             positions.data_ptr(), axes, inv_freq.data_ptr(), rot, pair_axis, 1 if interleaved else 0, out.data_ptr(),
-             out.stride(0), _at(gq), _at(gk), 1 if accumulate is not None else 0, _at(workspace),
-             0 if workspace is None else _scratch(workspace, dev))
+    _checked(dev, "qk_norm_rope_backward", dq.data_ptr(), qt, qh, dk.data_ptr(), kt, kh, _at(qkv), ld, tokens, heads_q,
+             heads_k, head_dim, _at(gamma_q), _at(gamma_k), eps, positions.data_ptr(), axes, inv_freq.data_ptr(), rot,
+             pair_axis, 1 if interleaved else 0, out.data_ptr(), out.stride(0), _at(gq), _at(gk),
+             1 if accumulate is not None else 0, _at(workspace), 0 if workspace is None else _scratch(workspace, dev))
     return QKNormGrads(out, gq, gk)

@@ -678,6 +678,9 @@ mxq_status qk_norm_rope_backward(const uint16_t* dq_bf16, int64_t dq_token_strid
     if (dgamma_q) {
         if (!workspace || workspace_bytes < qk_norm_backward_ws(head_dim)) return MXQ_ERR_WORKSPACE;
         if (!al16(workspace)) return MXQ_ERR_ALIGN;
+        // the two sums are written, or added, side by side
+        const uintptr_t gq = reinterpret_cast<uintptr_t>(dgamma_q), gk = reinterpret_cast<uintptr_t>(dgamma_k);
+        if ((gq < gk ? gk - gq : gq - gk) < (uintptr_t)head_dim * 4u) return MXQ_ERR_UNSUPPORTED;
     }
     a.dx = dqkv_bf16;
     a.lddx = ld_d;

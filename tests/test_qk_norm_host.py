@@ -89,3 +89,9 @@ def test_formula_gradient_against_differences(norm, interleaved):
         v = r(dim)
         assert abs((loss(qkv, gq + h * v, gk) - loss(qkv, gq - h * v, gk)) / (2 * h) - float((dgq * v).sum())) < 1e-5
         assert abs((loss(qkv, gq, gk + h * v) - loss(qkv, gq, gk - h * v)) / (2 * h) - float((dgk * v).sum())) < 1e-5
+
+
+def test_gradients_of_both_gammas_in_one_buffer_are_refused():
+    for dgk in (P, P + 16, P + 4 * 64 - 16, P - 16):
+        for acc in (0, 1):
+            assert _backward(dgk=dgk, acc=acc) == 4, (hex(dgk), acc)
