@@ -1032,9 +1032,9 @@ static Int8Plan int8_plan(int64_t M, int64_t cols, int64_t K, int64_t G, bool sw
         p.rows = M <= 16 * groups ? 16 : M <= 32 * groups ? 32 : 64;
         p.blocks = count(p.rows, p.rows == 16 || swiglu ? 16 : 32);
     // Three middle tiles a CU are as much as the large ones take for one round. Middle and large at 400 x 12288 x 12288: 117 and
-    // 122 us, 512 rows 129 and 124, 768 195 and 125, 160 x 36864 x 12288 176 and 149; 64 experts of 64 rows, up 70 and 77, of 88
-    // rows 85 and 78.
-    } else if (middle >= 768 && M >= 80 * groups) {
+    // 118 us, 300 rows 94 and 117, 512 rows 129 and 123, 768 194 and 124, 160 x 36864 x 12288 209 and 141; 64 experts, up to
+    // 2048 x 2048 with SwiGLU, 64 rows each (one middle tile) 69 and 76, 72 rows 82 and 77, 88 rows 84 and 73.
+    } else if (middle >= 768 && (G ? M > 64 * groups : M >= 80)) {
         p.kind = INT8_LARGE;
         p.rows = LT;
         p.blocks = count(LT, swiglu ? LT / 2 : LT);

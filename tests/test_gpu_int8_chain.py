@@ -157,3 +157,42 @@ def test_on_another_stream_and_into_the_training_path():
     mx = mxq.mx_quantize(r.dqk)                                            # the projection's dgrad and Wgrad operand
     back = mx.q_row.view(torch.float8_e4m3fn).float().view(T, -1, 32) * torch.exp2(mx.s_row.float() - 127)[..., None]
     assert float((back.view(T, -1) - dqkv.float()).norm() / dqkv.float().norm()) < 2.0 ** -4
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_large_products_side_by_side_and_replayed(swiglu):
+    """Products whose workgroups hold whole CUs, on two streams at once and from two graphs of the same buffers: the same
+    bytes as alone (the sums are exact)."""
+    need_gpu()
+    g = torch.Generator(device=DEV).manual_seed(5)
+    M, N, K, G = 2300, 8200, 416, 9
+    c = lambda *s: torch.randint(-128, 128, s, generator=g, device=DEV, dtype=torch.int32).to(torch.int8)  # noqa: E731
+    sc = lambda *s: torch.rand(s, generator=g, device=DEV) * 1e-4 + 1e-6  # noqa: E731
+    a, sa, b, sb = c(M, K), sc(M), c(G, N, K), sc(G, N)
+    off = torch.tensor([0, 0, 300, 301, 900, 1400, 1656, 2000, 2000, M], device=DEV)
+    dense = lambda: mxq.int8_scaled_gemm(a, sa, b[1], sb[1], swiglu=swiglu)  # noqa: E731
+    routed = lambda: mxq.int8_grouped_gemm(a, sa, off, b, sb, swiglu=swiglu)  # noqa: E731
+    say("large products side by side", swiglu)
+    want_d, want_r = dense(), routed()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (s1, s2):
+        s.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            got.append((dense(), want_d))
+        with torch.cuda.stream(s2):
+            got.append((routed(), want_r))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got)
+    graphs = []
+    for f in (dense, routed):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = f()
+        graphs.append((graph, out, f))
+    for _ in range(3):
+        a.copy_(c(M, K))
+        for graph, out, f in graphs:
+            graph.replay()
+            assert torch.equal(out, f())
