@@ -470,9 +470,9 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 
 // ---------------------------------------------------------------------------------------------------------------
 // Large tiles: 256 x 256 rows of A and B, one workgroup per CU, which takes its tiles in turn (LargeTiles); 4 waves, 2 x 2, each
-// 128 x 128 as 8 x 8 accumulators of 16 x 16 (256 registers). K advances 64 bytes per stage: one v_mfma_i32_16x16x64_i8 per accumulator.
-// (The chip is held back by its power here: from registers alone, on normally distributed codes, this instruction runs
-// at 4.2 POP/s and the 32 x 32 x 32 form at 3.4; on zeros both reach 4.9.) Operand of lane l: row l % 16, bytes 16 (l / 16)
+// 128 x 128 as 8 x 8 accumulators of 16 x 16 (256 registers). K advances 64 bytes per stage: one v_mfma_i32_16x16x64_i8 per
+// accumulator. (The chip is held back by its power here: from registers alone, on normally distributed codes, this instruction
+// runs at 4.2 POP/s and the 32 x 32 x 32 form at 3.4; on zeros both reach 4.9.) Operand of lane l: row l % 16, bytes 16 (l / 16)
 // .. + 15; B is the first operand, so register e of lane l holds output row l % 16, column 4 (l / 16) + e.
 //
 // K advances in pairs of stages, 128 bytes, so that a copy instruction (global to LDS, no registers) takes whole lines: 8
@@ -483,12 +483,13 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // lies behind its first trip, where every wave has read the whole pair p: trip 2p + 1 then copies B's pair p + 2 into B's
 // region of p, trip 2p + 2 A's pair p + 3 into A's region of p. At the next barrier, behind trip 2p + 2, all but that last
 // pair of A must have landed: B has one to two trips to arrive, A three to four.
-// The pairs of a workgroup's tiles are one sequence: while a tile's last pairs are multiplied the next tile's first are copied, and
-// they land while its outputs are computed and stored. (With a workgroup for each tile, the search for the tile, the first pairs and
-// the scales took 11,000 of 44,000 cycles at K = 1024, where the trips take 23,000.)
-// Measured: 4096 x 36864 x 12288 1.20 to 1.23 ms, 3.0 POP/s (1.22 to 1.26 with a workgroup for each tile); 131072 rows of 64 experts,
-// K = 2048 to 2 x 1024 with SwiGLU 473 to 484 us, 2.3 POP/s (522), K = 1024 to 2048 307 to 313 us, 1.8 POP/s (357). What is left of a tile beside its
-// trips is mostly the arithmetic on the sums, 8,000 cycles (with SwiGLU 10,000), for which the matrix unit waits.
+// The pairs of a workgroup's tiles are one sequence: while a tile's last pairs are multiplied the next tile's first are copied,
+// and they land while its outputs are computed and stored. (With a workgroup for each tile, the search for the tile, the first
+// pairs and the scales took 11,000 of 44,000 cycles at K = 1024, where the trips take 23,000.)
+// Measured: 4096 x 36864 x 12288 1.20 to 1.23 ms, 3.0 POP/s (1.22 to 1.26 with a workgroup for each tile); 131072 rows of 64
+// experts, K = 2048 to 2 x 1024 with SwiGLU 473 to 484 us, 2.3 POP/s (522), K = 1024 to 2048 307 to 313 us, 1.8 POP/s (357). What
+// is left of a tile beside its trips is mostly the arithmetic on the sums, 8,000 cycles (with SwiGLU 10,000), for which the
+// matrix unit waits.
 constexpr int LT = 256, LPAIR = 128, LREGION = LT * LPAIR, LREGIONS_A = 3;
 
 typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
@@ -499,8 +500,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int r
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, records, 0x00020000);
 }
 
-// acc += b a, and acc = b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the instruction
-// another destination and copies results about in the loop. The operands' loads are waited for by the compiler; nothing
+// acc += b a, and acc = b a. Written as assembly so that the sum stays in its registers: left to itself the compiler gives the
+// instruction another destination and copies results about in the loop. The operands' loads are waited for by the compiler; nothing
 // else may write an operand or read a sum within 19 wait states (the kernel has 64 instructions between two uses of a
 // sum, and waits of its own around the last stage).
 __device__ __forceinline__ void mfma_in_place(v4i& acc, v4i b, v4i a) {
@@ -619,8 +620,8 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
         return t.grp < 0 ? buffer_rsrc(g.a, 0) : rows_rsrc(g.a + t.m0 * g.K, g.M - t.m0, g.K);
     };
     auto b_rows = [&](const Int8Tile& t) {                      // SwiGLU: waves 0, 1 bring gate rows, waves 2, 3 up rows
-        const int64_t n0 = t.n * TC;
-        return t.grp < 0 ? buffer_rsrc(g.b, 0) : rows_rsrc(g.b + (t.grp * g.N + n0 + (SWIGLU && wave >= 2 ? cols : 0)) * g.K, cols - n0, g.K);
+        const int64_t n0 = t.n * TC, row = t.grp * g.N + n0 + (SWIGLU && wave >= 2 ? cols : 0);
+        return t.grp < 0 ? buffer_rsrc(g.b, 0) : rows_rsrc(g.b + row * g.K, cols - n0, g.K);
     };
     const int brow = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ (4 * (wave & 1) + (lane >> 4));
     const int K = (int)g.K;
@@ -631,7 +632,8 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
     // Pairs of a tile: at least three, so that copies reach no further ahead than the next tile; a shorter contraction is filled up
     // with pairs whose A is zeros. What the last pair holds past the end of K is zeros in A too (an offset out of range).
     const int pairs = (K + LPAIR - 1) / LPAIR, np = max(pairs, 3), fill = np - pairs;
-    const int a_none = 0x7F000000, a_last = 16 * chunk < K - LPAIR * (pairs - 1) ? a_off : a_none, a_first = pairs == 1 ? a_last : a_off;
+    const int a_none = 0x70000000, a_last = 16 * chunk < K - LPAIR * (pairs - 1) ? a_off : a_none;
+    const int a_first = pairs == 1 ? a_last : a_off;
     // The pairs of one operand in the order they are copied: a tile's, then the next tile's. Behind the last tile an empty operand.
     struct Stream {
         v4i rows;
@@ -764,18 +766,18 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
         }
 
         // -------------------------------------------------------------- scales of the wave's rows and columns
-        // Read ahead of the last trip. A whole tile's come by addresses that differ by constants; an address, a clamp and a check
-        // for each cost more than the arithmetic on the sums (a wave is alone on its SIMD here, four cycles an instruction).
+        // Read ahead of the last trip, at addresses that differ by constants: an address, a clamp and a check for each cost more
+        // than the arithmetic on the sums (a wave is alone on its SIMD here, four cycles an instruction).
         const int64_t m0 = tile.m0, m_end = tile.m_end, n0 = tile.n * TC, grp = tile.grp;
         const int64_t n_end = n0 + TC < cols ? n0 + TC : cols;
-        constexpr int NB = SWIGLU ? 4 : 8;                          // 16-column output blocks of a wave
+        constexpr int NB = SWIGLU ? 4 : 8;                      // 16-column output blocks of a wave
         const float* sb = g.sb + grp * g.N + n0 + wn * (TC / 2);
         const float* sm = g.sa + m0 + wm * 128;
         float sa[8];
         f32x4a s_gate[NB], s_up[SWIGLU ? NB : 1];
         const int rows_left = (int)(m_end - m0) - wm * 128, cols_left = (int)(n_end - n0) - wn * (TC / 2);    // of the wave
         if constexpr (ALIGNED) {
-            // bytes behind a tile's last row or column are out of the buffer's range and read as zeros
+            // those behind a tile's last row or column are out of the buffer's range and read as zeros
             const auto ra = buffer_of(sm, 4 * max(rows_left, 0)), rg = buffer_of(sb, 4 * max(cols_left, 0));
             const auto ru = buffer_of(sb + cols, SWIGLU ? 4 * max(cols_left, 0) : 0);
 #pragma unroll
@@ -833,7 +835,7 @@ __global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
         uint16_t* dst = g.c + (m0 + wm * 128) * g.ldc + n0 + wn * (TC / 2);
         if constexpr (ALIGNED) {
             const uint32_t row_bytes = 2 * (uint32_t)g.ldc;
-            const auto rc = buffer_of(dst, (int)(max(rows_left, 0) * row_bytes));              // rows behind the last are left as they were
+            const auto rc = buffer_of(dst, (int)(max(rows_left, 0) * row_bytes));      // rows behind the last stay as they were
             uint32_t at[NB / 2];
 #pragma unroll
             for (int p = 0; p < NB / 2; ++p) at[p] = col0 + 32 * p < cols_left ? r16 * row_bytes + 2 * (col0 + 32 * p) : 0x7F000000u;
@@ -901,7 +903,8 @@ __global__ __launch_bounds__(64 * FEW_W) void int8_few_kernel(Int8Gemm g) {
     const int r16 = lane & 15, q16 = lane >> 4;
     for (int i = tid; i < 16 * NT * PITCH; i += 64 * W) (&sums[0][0])[i] = 0;
 
-    // The wave's steps are its pieces wave + W i of 128 bytes, from a place of the workgroup's own on. Copies of steps past the last ask for a place behind the operands.
+    // The wave's steps are its pieces wave + W i of 128 bytes, from a place of the workgroup's own on. Copies of steps past the
+    // last ask for a place behind the operands.
     // Rows behind an operand's end, and bytes past K, are zeros or a neighbour's: the sums of the first are not stored, the
     // second are masked in A.
     const int8_t* B = g.b + (grp * g.N + n0) * g.K;
