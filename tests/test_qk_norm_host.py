@@ -2,6 +2,7 @@
 their gradient against differences."""
 import ctypes as C
 
+import numpy as np
 import pytest
 import torch
 
@@ -95,3 +96,14 @@ def test_gradients_of_both_gammas_in_one_buffer_are_refused():
     for dgk in (P, P + 16, P + 4 * 64 - 16, P - 16):
         for acc in (0, 1):
             assert _backward(dgk=dgk, acc=acc) == 4, (hex(dgk), acc)
+
+
+@pytest.mark.parametrize("kind", [list, bytes, np.array, torch.tensor, lambda v: torch.tensor(v, dtype=torch.uint8)])
+def test_pair_axis_from_any_sequence(kind):
+    """An array of 64-bit numbers is a sequence of its numbers, not of their bytes."""
+    want = [0] * 8 + [1] * 12 + [2] * 12
+    pos, inv = torch.zeros(3, 4, dtype=torch.int64), torch.ones(32)
+    axes, rot, got = mxq._expect_rotation(4, pos, inv, kind(want), None, None, 64, pos.device)
+    assert (axes, rot, list(got)) == (3, 64, want)
+    with pytest.raises(ValueError):
+        mxq._expect_rotation(4, pos, inv, kind(want[1:]), None, None, 64, pos.device)
