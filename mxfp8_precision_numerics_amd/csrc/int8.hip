@@ -5,10 +5,10 @@
 //   product:   C[m][n] = bf16( (sum_k a[m][k] b[n][k]) sa[m] sb[n] ),  the sum exact in 32-bit integers
 //   SwiGLU:    B holds F gate rows, then F up rows:  C[m][f] = bf16( silu(G[m][f]) U[m][f] ) from the products in fp32
 #pragma clang fp contract(off)
-#include <algorithm>
 #include <type_traits>
 
 #include "gemm_tile.h"
+#include "int8_plan.h"
 #include "launch.h"
 #include "mx_block.h"
 
@@ -169,7 +169,6 @@ struct Int8Tile {
 };
 constexpr int GROUP_M = 4;              // row tiles that an XCD's workgroups walk together
 constexpr int64_t XCD_CHUNK = 32;       // consecutive tiles that an XCD takes at a time (grouped)
-constexpr int CUS = 256;                // of the chip
 
 template <int TM, bool GROUPED>
 __device__ __forceinline__ Int8Tile tile_of(const Int8Gemm& g, int tiles_n) {
@@ -216,7 +215,6 @@ __device__ __forceinline__ v4i rows_rsrc(const int8_t* p, int64_t rows, int64_t 
 // every wave and the one before it has been read, so its place is filled with the stage DEPTH - 1 ahead. B is the instruction's
 // first operand: lane l, register e hold output row l % 16, column 4 (l / 16) + e. (128 x 128 tiles, two to a CU, were within
 // 5% of the better of these and the large ones, or behind, at 130 to 2048 rows.)
-constexpr int MT_M = 64, MT_N = 128;
 template <int DEPTH, bool GROUPED, bool SWIGLU>
 __global__ __launch_bounds__(256) void int8_gemm_kernel(Int8Gemm g) {
     constexpr int STAGE = (MT_M + MT_N) * 128, COPIES = STAGE / 4096;            // copies of a wave
@@ -490,7 +488,7 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // experts, K = 2048 to 2 x 1024 with SwiGLU 473 to 484 us, 2.3 POP/s (522), K = 1024 to 2048 307 to 313 us, 1.8 POP/s (357). What
 // is left of a tile beside its trips is mostly the arithmetic on the sums, 8,000 cycles (with SwiGLU 10,000), for which the
 // matrix unit waits.
-constexpr int LT = 256, LPAIR = 128, LREGION = LT * LPAIR, LREGIONS_A = 3;
+constexpr int LPAIR = 128, LREGION = LT * LPAIR, LREGIONS_A = 3;
 
 typedef float f32x4a __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -515,19 +513,19 @@ __device__ __forceinline__ void mfma_from_zero(v4i& acc, v4i b, v4i a) {
 // The tiles that one workgroup takes in turn: every gridDim.x-th of an order in which each XCD (every eighth workgroup) walks a
 // contiguous run, so that the workgroups of an XCD share rows and weights in its L2. Grouped: a wave holds the rows of 64 groups
 // and the number of row tiles before each, a group a lane, and the next tile costs no memory access until one lies behind those.
+// The walk over the groups goes forward only, so a workgroup's tiles must not decrease: int8_plan.h says why they do not.
 template <bool GROUPED>
 struct LargeTiles {
     const Int8Gemm& g;
     const int tiles_n;
-    int tiles_m, T, b = blockIdx.x;
+    int tiles_m, T, b = blockIdx.x;     // tiles_m: dense only
     int64_t base = 0, lo = 0, hi = 0;   // lane l: rows of group base + l
     int before = 0, excl = 0, total = 0;
 
-    __device__ __forceinline__ LargeTiles(const Int8Gemm& g_, int tn) : g(g_), tiles_n(tn) {
-        int64_t rows;
+    __device__ __forceinline__ LargeTiles(const Int8Gemm& g_, int tn, int most) : g(g_), tiles_n(tn) {
         if constexpr (GROUPED) {
             load();
-            rows = total;
+            int64_t rows = total;
             if (g.G > 64) {
                 for (base = 64; base < g.G; base += 64) {
                     load();
@@ -536,11 +534,11 @@ struct LargeTiles {
                 base = 0;
                 load();
             }
+            T = large_tiles(rows, tiles_n, most);
         } else {
-            rows = (g.M + LT - 1) / LT;
+            tiles_m = (int)((g.M + LT - 1) / LT);
+            T = tiles_m * tiles_n;
         }
-        tiles_m = (int)(rows < 0x7FFFFFFF / tiles_n ? rows : 0x7FFFFFFF / tiles_n);
-        T = tiles_m * tiles_n;
     }
     __device__ __forceinline__ void load() {
         const int lane = threadIdx.x & 63;
@@ -569,7 +567,7 @@ struct LargeTiles {
     __device__ __forceinline__ Int8Tile next() {
         Int8Tile r{0, 0, -1, 0};
         if (b >= T) return r;
-        const int T8 = T & ~7, v = b < T8 ? (b & 7) * (T8 >> 3) + (b >> 3) : b;
+        const int v = large_tile(b, T);
         b += (int)gridDim.x;
         if constexpr (GROUPED) {
             const int row = v / tiles_n;
@@ -600,14 +598,14 @@ struct LargeTiles {
 };
 
 template <bool GROUPED, bool SWIGLU, bool ALIGNED>
-__global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g) {
+__global__ __launch_bounds__(256, 1) void int8_gemm_large_kernel(Int8Gemm g, int most) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[(LREGIONS_A + 2) * LREGION];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave & 1, wn = wave >> 1;
     const int64_t cols = SWIGLU ? g.N / 2 : g.N;
     constexpr int TC = SWIGLU ? LT / 2 : LT;
-    LargeTiles<GROUPED> tiles(g, (int)((cols + TC - 1) / TC));
+    LargeTiles<GROUPED> tiles(g, (int)((cols + TC - 1) / TC), most);
     Int8Tile tile = tiles.next();
     if (tile.grp < 0) return;
     const int r16 = lane & 15, q16 = lane >> 4;
@@ -989,69 +987,6 @@ __global__ __launch_bounds__(64 * FEW_W) void int8_few_kernel(Int8Gemm g) {
     }
 }
 
-// Upper bound of the row tiles of TH rows over ragged groups: every group with rows adds at most one partial tile.
-static int64_t most_row_tiles(int64_t rows, int64_t G, int64_t TH) { return (rows + TH - 1) / TH + (G < rows ? G : rows); }
-
-// Which kernel takes a call, and its grid. The rules are on the rows of A (for each expert, on average) and on sizes that say how
-// many workgroups the middle tiles would make; the times are of one call, us, at rows x N x K.
-enum : int { INT8_FEW, INT8_WIDE, INT8_MIDDLE, INT8_LARGE };
-struct Int8Plan {
-    int kind, rows;             // rows of A in a tile
-    int wide;                   // 16-row blocks of B in a wide tile
-    bool deep;                  // middle tiles: the longer ring
-    int64_t blocks;
-};
-
-static Int8Plan int8_plan(int64_t M, int64_t cols, int64_t K, int64_t G, bool swiglu) {
-    Int8Plan p{};
-    const int64_t groups = G ? G : 1, N = swiglu ? 2 * cols : cols;
-    auto count = [&](int64_t th, int64_t tc) {
-        const int64_t tn = (cols + tc - 1) / tc, tm = G ? most_row_tiles(M, G, th) : (M + th - 1) / th;
-        return tn > 0 && tm > INT64_MAX / tn ? INT64_MAX : tm * tn;
-    };
-    const int64_t middle = count(MT_M, swiglu ? MT_N / 2 : MT_N), weight = N * K;
-    // One dense pass over weights of 96 MB and more (128 MB for up to 32 tokens, 256 MB for up to 16, as fewer tokens leave less
-    // to share): wide tiles, where N makes two blocks a CU. Wide and few at 16 x 36864 x 12288: 79 and 90 us, 61 rows 88 and 132;
-    // at 32 x 12288 x 12288 32 and 38, 61 rows 40 and 50; but 16 rows 33 and 31, and at 61 x 8192 x 8192 21 and 15.
-    if (!G && M > 4 && M <= 128 && N >= 8192 && weight >= (M <= 16 ? 256000000 : M <= 32 ? 128000000 : 96000000)) {
-        p.kind = INT8_WIDE;
-        p.rows = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-        const int64_t units = (cols + 15) / 16;
-        int64_t best = INT64_MAX;
-        for (int k = 1; k <= (swiglu ? 6 : 12); ++k) {
-            const int b = swiglu ? 2 * k : k;
-            const int64_t cost = ((units + k - 1) / k + 255) / 256 * (b + p.rows / 16);
-            if (cost <= best) {
-                best = cost;
-                p.wide = b;
-            }
-        }
-        p.blocks = count(p.rows, (swiglu ? 8 : 16) * (int64_t)p.wide);
-    // Up to 8 rows an expert (64 dense ones), or so few middle tiles that half the CUs had none: the contraction is shared within
-    // a workgroup. Few and middle at 100 x 6144 x 2048: 11 and 13 us, 256 x 2048 x 8192 13 and 34, 200 x 6144 x 2048 17 and 14;
-    // 64 experts, up to 2048 x 2048 with SwiGLU: 16 rows an expert 65 and 60, 32 86 and 63.
-    } else if (M <= (G ? 8 * groups : 64) || middle <= 128) {
-        p.kind = INT8_FEW;
-        p.rows = M <= 16 * groups ? 16 : M <= 32 * groups ? 32 : 64;
-        p.blocks = count(p.rows, p.rows == 16 || swiglu ? 16 : 32);
-    // Three middle tiles a CU are as much as the large ones take for one round. Middle and large at 400 x 12288 x 12288: 117 and
-    // 118 us, 300 rows 94 and 117, 512 rows 129 and 123, 768 194 and 124, 160 x 36864 x 12288 209 and 141; 64 experts, up to
-    // 2048 x 2048 with SwiGLU, 64 rows each (one middle tile) 69 and 76, 72 rows 82 and 77, 88 rows 84 and 73.
-    } else if (middle >= 768 && (G ? M > 64 * groups : M >= 80)) {
-        p.kind = INT8_LARGE;
-        p.rows = LT;
-        p.blocks = count(LT, swiglu ? LT / 2 : LT);
-    // Three stages, two workgroups a CU, while these hold all tiles; two stages, three workgroups, beyond: at 130 x 12288 x 12288
-    // 81 and 91 us, at 400 rows 142 and 117.
-    } else {
-        p.kind = INT8_MIDDLE;
-        p.rows = MT_M;
-        p.blocks = middle;
-        p.deep = middle <= 512;
-    }
-    return p;
-}
-
 bool int8_gemm_fits(int64_t M, int64_t cols, int64_t K, int64_t G, int swiglu) {
     return int8_plan(M, cols, K, G, swiglu != 0).blocks <= kMaxThreads / 256;
 }
@@ -1073,9 +1008,9 @@ static void launch_products(const Int8Gemm& g, int64_t cols, hipStream_t stream)
     const dim3 blocks((unsigned)p.blocks), threads(256);
     // 16-byte stores by 32-bit offsets within a tile
     const bool aligned = cols % 8 == 0 && g.ldc % 8 == 0 && g.ldc < (1 << 21) && (reinterpret_cast<uintptr_t>(g.c) & 15) == 0;
-    const dim3 cus((unsigned)std::min<int64_t>(p.blocks, CUS));
-    if (p.kind == INT8_LARGE && aligned) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU, true>), cus, threads, 0, stream, g);
-    else if (p.kind == INT8_LARGE) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU, false>), cus, threads, 0, stream, g);
+    const dim3 cus((unsigned)large_groups(p.blocks));
+    if (p.kind == INT8_LARGE && aligned) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU, true>), cus, threads, 0, stream, g, (int)p.blocks);
+    else if (p.kind == INT8_LARGE) hipLaunchKernelGGL((int8_gemm_large_kernel<GROUPED, SWIGLU, false>), cus, threads, 0, stream, g, (int)p.blocks);
     else if (p.kind == INT8_MIDDLE && p.deep) hipLaunchKernelGGL((int8_gemm_kernel<3, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
     else if (p.kind == INT8_MIDDLE) hipLaunchKernelGGL((int8_gemm_kernel<2, GROUPED, SWIGLU>), blocks, threads, 0, stream, g);
     else if (p.kind == INT8_WIDE && p.wide <= 4) launch_wide<4, SWIGLU>(g, p, stream);
