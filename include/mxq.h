@@ -446,7 +446,8 @@ mxq_status int8_quantize_tokens(const uint16_t* x_bf16, int64_t rows, int64_t co
  *   s[m][n] = sum_k a_q[m][k] b_q[n][k], exact;  y[m][n] = (fp32(s) a_scale[m]) b_scale[n], each operation one fp32 rounding;
  *   swiglu == 0: c_bf16[M][N] = bf16_rne(y);
  *   swiglu != 0: N = 2F, B holds the F gate rows, then the F up rows:  c_bf16[M][F] = bf16_rne(silu(g) u) with
- *   g = y[m][f], u = y[m][F + f] in fp32 and silu(g) = g / (1 + e^-g) within (13 + 2 |g|) 2^-24 of itself.
+ *   g = y[m][f], u = y[m][F + f] in fp32 and silu(g) = g / (1 + e^-g) within (13 + 2 |g|) 2^-24 of itself for g >= -87. Below
+ *   that, where |silu(g)| < 2^-119, it may come out as 0.
  * Both operands are K-contiguous; rows of c_bf16 have stride ldc >= its columns. Any codes (-128 too) and any M and N (N even
  * with swiglu). Requires K % 32 == 0 and 0 < K < 131072 (every sum then fits 32 bits). c_bf16 needs 2-byte and the scales
  * 4-byte alignment. A result does not depend on M, on the row's place, or on timing: the sum is exact. No workspace.
