@@ -486,7 +486,7 @@ mxq_status int8_grouped_gemm(const int8_t* a_q, const float* a_scale, const int6
  * Requires head_dim a multiple of 16 up to 256, rot a multiple of 16 up to head_dim (0: no rotation), 1 <= axes <= 4,
  * pair_axis[i] < axes, 0 <= heads <= 65536, tokens <= 2^25,
  * tokens * (heads_q + heads_k) <= 2^31, ld and the strides (where there is more than one token or
- * head) multiples of 8, ld at least the heads' width, strides at least head_dim, and 0 < eps < 3e38 with a norm. positions
+ * head) multiples of 8, ld at least the heads' width, strides at least head_dim, and 2^-126 <= eps < 3e38 with a norm. positions
  * needs 8-byte and inv_freq 4-byte alignment.
  */
 mxq_status qk_norm_rope(const uint16_t* qkv_bf16, int64_t ld, int64_t tokens, int64_t heads_q, int64_t heads_k,

@@ -38,7 +38,8 @@ mxq_status qk_args(const uint16_t* x, int64_t ld, int64_t tokens, int64_t hq, in
                    int64_t rot, const uint8_t* pair_axis, int interleaved, uint16_t* q, int64_t q_token, int64_t q_head,
                    uint16_t* k, int64_t k_token, int64_t k_head, mxq::QkArgs& a) {
     if ((gamma_q == nullptr) != (gamma_k == nullptr)) return MXQ_ERR_NULL;
-    if (gamma_q && !(eps > 0.0f && eps < 3.0e38f)) return MXQ_ERR_UNSUPPORTED;                  // NaN fails too
+    // NaN fails too; v_rsq_f32 takes a subnormal mean of squares as zero, which a zero head would meet below FLT_MIN
+    if (gamma_q && !(eps >= 0x1p-126f && eps < 3.0e38f)) return MXQ_ERR_UNSUPPORTED;
     if (tokens < 0 || tokens > (int64_t(1) << 25) || hq < 0 || hk < 0 || hq > 65536 || hk > 65536) return MXQ_ERR_SHAPE;
     if (tokens * (hq + hk) > (int64_t(1) << 31)) return MXQ_ERR_SHAPE;                          // 32-bit counts of work
     if (dim < 16 || dim > mxq::kQkMaxDim || dim % 16 != 0 || rot < 0 || rot > dim || rot % 16 != 0) return MXQ_ERR_SHAPE;
