@@ -38,10 +38,11 @@ __device__ __forceinline__ Int8Row int8_row(uint32_t amax_bits) {
     return r;
 }
 
-// The code of x in the low byte. t = x inv is within 2^-23 t of 127 x / amax. That quotient of two 8-bit significands is
-// either exactly halfway between two codes or at least 2^-15 t away from it, so t rounded to 18 significant bits falls on
-// the half exactly where the quotient does, and on the quotient's side of it elsewhere: the code is the quotient's own,
-// without a division. Adding 1.5 2^23 rounds to the integer, ties to even, and leaves it in the low bits.
+// The code of x in the low byte. t = x inv is within 2^-23 t of 127 x / amax. With 8-bit significands X and A, that quotient and a
+// half between two codes differ by a whole multiple of 1 / 2A in the binade of x, or not at all: by at least t / (254 X) > 2^-16 t.
+// t rounded to 18 significant bits moves by at most 2^-18 t, so it falls on the half exactly where the quotient does, and on the
+// quotient's side of it elsewhere: the code is the quotient's own, without a division. Adding 1.5 2^23 rounds to the integer,
+// ties to even, and leaves it in the low bits.
 __device__ __forceinline__ uint32_t int8_code(float x, const Int8Row& r) {
     const float t = (x * r.pre) * r.inv;
     const float u = __uint_as_float((__float_as_uint(t) + 0x20u) & ~0x3Fu);
