@@ -436,7 +436,7 @@ size_t moe_mx_few_tokens_workspace_bytes(int64_t tokens, int64_t experts, int64_
  *   -127 <= q <= 127 and x ~ q scale.
  * An all-zero row has scale 0 and zero codes; a row holding a NaN or an infinity has a NaN scale and zero codes, so that
  * every product with it is NaN. Requires cols % 32 == 0, and rows * t <= 2^32 - 1024 with t = 64 up to 2048 columns, 256 up
- * to 8192 and 1024 beyond. scale needs 4-byte alignment.
+ * to 8192 and 1024 beyond. With no columns nothing is written, scale neither. scale needs 4-byte alignment.
  */
 mxq_status int8_quantize_tokens(const uint16_t* x_bf16, int64_t rows, int64_t cols, int8_t* q, float* scale,
                                 hipStream_t stream);

@@ -707,6 +707,8 @@ def int8_quantize_tokens(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> I
         _expect(out.q, (rows, cols), torch.int8, dev, "out.q")
         _expect(out.scale, (rows,), torch.float32, dev, "out.scale")
     _checked(dev, "int8_quantize_tokens", x.data_ptr(), rows, cols, out.q.data_ptr(), out.scale.data_ptr())
+    if cols == 0:                                                  # the library writes nothing; rows without values are zero
+        out.scale.zero_()
     return out
 
 
