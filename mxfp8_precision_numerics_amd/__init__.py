@@ -863,7 +863,7 @@ def qk_norm_rope_backward(dq: torch.Tensor, dk: torch.Tensor, qkv: Optional[torc
     else:
         _expect_rows(out, tokens, width, dev, "out")
     gq = gk = None
-    if gamma_q is not None and accumulate is not None:
+    if gamma_q is not None and want_dgamma and accumulate is not None:
         gq, gk = accumulate
         _expect(gq, (head_dim,), torch.float32, dev, "accumulate[0]")
         _expect(gk, (head_dim,), torch.float32, dev, "accumulate[1]")
