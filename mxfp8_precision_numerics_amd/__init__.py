@@ -787,8 +787,8 @@ def _expect_rotation(tokens: int, positions: torch.Tensor, inv_freq: torch.Tenso
     if pair_axis is not None:
         if len(pair_axis) != pairs:
             raise ValueError("pair_axis must name one axis for each of inv_freq's pairs")
-        # an array would hand bytes() its memory
-        pair_axis = bytes(pair_axis if isinstance(pair_axis, (bytes, list, tuple)) else [int(a) for a in pair_axis])
+        # an array would hand bytes() its memory; of a list it takes whole numbers only
+        pair_axis = bytes(pair_axis if isinstance(pair_axis, (bytes, list, tuple)) else list(pair_axis))
     return axes, 2 * pairs, pair_axis
 
 
