@@ -479,7 +479,8 @@ mxq_status int8_grouped_gemm(const int8_t* a_q, const float* a_scale, const int6
  *     (a, b) -> (a cos - b sin, b cos + a sin);  values past rot are n.
  *   position = positions[pair_axis[i]][token]: positions is a device int64[axes][tokens] (time, height and width of images and
  *   video, say), pair_axis a HOST array of rot / 2 bytes (NULL: axis 0 for all). inv_freq is a device fp32[rot / 2]. Angles are
- *   reduced in 64 bits with the products' roundings kept: cos and sin are within 2^-23 for |position inv_freq| < 2^50.
+ *   reduced in 64 bits with the products' roundings kept: cos and sin are within 2^-23 for |position| <= 2^53 and
+ *   |position inv_freq| < 2^50.
  * Value d of head h of token t goes to q_bf16[t q_token_stride + h q_head_stride + d], keys likewise: token-major, head-major
  * or rows of a cache. The outputs may be the heads' own places in qkv_bf16 (in place).
  * A NaN in a head makes the head NaN with a norm, its pair without; where squares overflow fp32, rstd is 0.

@@ -20,7 +20,8 @@
 namespace mxq {
 
 // cos and sin of pos * w. The angle is formed in quarter turns in 64 bits with the products' own roundings kept, so what is
-// left after the whole quarters is good to 2^-50 quarters for angles up to 2^50: positions may lie as far as they like.
+// left after the whole quarters is good to 2^-50 quarters for angles up to 2^50, as long as pos itself is a 64-bit floating-point
+// number (|pos| <= 2^53).
 // |r| <= 1/2 quarter; then the Taylor polynomials of degree 9 and 10, whose remainders are below 2^-28.
 __device__ __forceinline__ float2 cos_sin(int64_t pos, float freq) {
     const double p = (double)pos, w = (double)freq;
