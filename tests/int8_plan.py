@@ -19,6 +19,10 @@ int plan(int64_t M, int64_t cols, int64_t K, int64_t G, int swiglu, int64_t* blo
     *rows = p.rows;
     return p.kind;
 }
+int form(int64_t M, int64_t cols, int64_t K, int64_t G, int swiglu) {       // wide: few blocks of B; middle: the longer ring
+    const mxq::Int8Plan p = mxq::int8_plan(M, cols, K, G, swiglu != 0);
+    return p.kind == mxq::INT8_WIDE ? p.wide <= 4 : p.kind == mxq::INT8_MIDDLE ? p.deep : 0;
+}
 int groups(int64_t most) { return mxq::large_groups(most); }
 int tiles(int64_t row_tiles, int tiles_n, int most) { return mxq::large_tiles(row_tiles, tiles_n, most); }
 int tile(int b, int T) { return mxq::large_tile(b, T); }
@@ -38,6 +42,7 @@ def load(folder):
     assert r.returncode == 0, r.stderr
     lib = C.CDLL(lib)
     lib.plan.argtypes = [C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int, C.POINTER(C.c_int64), C.POINTER(C.c_int)]
+    lib.form.argtypes = [C.c_int64, C.c_int64, C.c_int64, C.c_int64, C.c_int]
     lib.groups.argtypes = [C.c_int64]
     lib.tiles.argtypes = [C.c_int64, C.c_int, C.c_int]
     return lib
@@ -48,3 +53,16 @@ def plan(lib, M, cols, K, G=0, swiglu=False):
     blocks, rows = C.c_int64(), C.c_int()
     kind = lib.plan(M, cols, K, G, 1 if swiglu else 0, C.byref(blocks), C.byref(rows))
     return kind, blocks.value, rows.value
+
+
+def variant(lib, M, cols, K, G=0, swiglu=False, aligned=True):
+    """The kernel's form that takes a call: all that tells the compiled ones apart. aligned: 16-byte rows of the output."""
+    kind, _, rows = plan(lib, M, cols, K, G, swiglu)
+    form = bool(lib.form(M, cols, K, G, 1 if swiglu else 0))
+    if kind == LARGE:
+        return "large", G > 0, swiglu, aligned and cols % 8 == 0
+    if kind == MIDDLE:
+        return "middle", form, G > 0, swiglu
+    if kind == WIDE:
+        return "wide", rows, form, swiglu
+    return "few", rows, G > 0, swiglu
