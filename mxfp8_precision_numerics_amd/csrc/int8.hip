@@ -487,8 +487,9 @@ __global__ __launch_bounds__(256) void int8_wide_kernel(Int8Gemm g, int blocks) 
 // The pairs of a workgroup's tiles are one sequence: while a tile's last pairs are multiplied the next tile's first are copied,
 // and they land while its outputs are computed and stored. (With a workgroup for each tile, the search for the tile, the first
 // pairs and the scales took 11,000 of 44,000 cycles at K = 1024, where the trips take 23,000.)
-// Measured: 4096 x 36864 x 12288 1.20 to 1.23 ms, 3.0 POP/s (1.22 to 1.26 with a workgroup for each tile); 131072 rows of 64
-// experts, K = 2048 to 2 x 1024 with SwiGLU 473 to 484 us, 2.3 POP/s (522), K = 1024 to 2048 307 to 313 us, 1.8 POP/s (357). What
+// Measured, over calls, boxes and what ran before (the chip's power): 4096 x 36864 x 12288 1.20 to 1.28 ms, 2.9 to 3.1 POP/s (1.22 to
+// 1.26 with a workgroup for each tile where these took 1.20); 131072 rows of 64 experts, K = 2048 to 2 x 1024 with SwiGLU 473 to 536
+// us, 2.1 to 2.3 POP/s (522 where these took 473), K = 1024 to 2048 307 to 320 us, 1.7 to 1.8 POP/s (357 against 307). What
 // is left of a tile beside its trips is mostly the arithmetic on the sums, 8,000 cycles (with SwiGLU 10,000), for which the
 // matrix unit waits.
 constexpr int LPAIR = 128, LREGION = LT * LPAIR, LREGIONS_A = 3;

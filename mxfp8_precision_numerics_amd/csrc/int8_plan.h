@@ -56,7 +56,8 @@ inline Int8Plan int8_plan(int64_t M, int64_t cols, int64_t K, int64_t G, bool sw
         p.blocks = count(p.rows, p.rows == 16 || swiglu ? 16 : 32);
     // Three middle tiles a CU are as much as the large ones take for one round. Middle and large at 400 x 12288 x 12288: 117 and
     // 118 us, 300 rows 94 and 117, 512 rows 129 and 123, 768 194 and 124, 160 x 36864 x 12288 209 and 141; 64 experts, up to
-    // 2048 x 2048 with SwiGLU, 64 rows each (one middle tile) 69 and 76, 72 rows 82 and 77, 88 rows 84 and 73.
+    // 2048 x 2048 with SwiGLU, 64 rows each (one middle tile) 69 and 76, 72 rows 82 and 77, 88 rows 84 and 73. Neither is near what
+    // weights (7.0 TB/s) and operations (3.0 POP/s) need there: 22 to 52 us for 130 to 512 rows of 12288 x 12288, about 41 for the experts.
     } else if (middle >= 768 && (G ? M > 64 * groups : M >= 80)) {
         p.kind = INT8_LARGE;
         p.rows = LT;
